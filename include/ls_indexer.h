@@ -476,6 +476,136 @@ ls_status ls_sparse_attention(const uint16_t* q, const uint16_t* latent, const i
 ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S, int64_t rows, int d_v, float* o,
                              float* lse, void* stream);
 
+/* output types of the span attentions */
+#define LS_OUT_F32 0
+#define LS_OUT_BF16 1
+
+/*
+ * ls_window_attention -- attention of query tokens over the sinks and the
+ * window of their sequences' latent rows ("Latent Sparse Attention", "The
+ * method, term by term", step 6: the sinks and the window are always read),
+ * in the absorbed MLA form of ls_sparse_attention: rows of 576 elements are
+ * every head's key, their first 512 the value.
+ *
+ * Sequence b has the query tokens q_start[b] .. q_start[b+1] - 1 and the
+ * kv_len[b] latent rows row_off[b] .. row_off[b] + kv_len[b] - 1, its query
+ * tokens' own rows last: token i of n is at position p = kv_len[b] - n + i.
+ * It sees row j of its sequence when j <= p and (j < n_sink or j >= lo), with
+ *   lo = max(0, p - window + 1) rounded down to a multiple of align.
+ * align = 1 is the sliding window of `window` rows, the token's own row
+ * included; window = 1 with align = the block length is the bucket search's
+ * window (a token's own, not yet clustered block), so that the result joins
+ * that of ls_sparse_attention over the long-range keys by ls_attention_merge.
+ *
+ *   q [T][H][576] bf16, latent [n_rows][576] bf16 (16-byte aligned)
+ *   q_start [B+1] int32 ascending, kv_len [B] int32, row_off [B] int64 or NULL
+ *   (zeros); H in [1, 1024]; T * H < 2^31
+ *   max_q: at least the longest sequence's query tokens (T is always enough;
+ *        the grid covers B * max_q tokens)
+ *   out [T][H][512], fp32 or bf16 by out_dtype (LS_OUT_*); lse [T][H] fp32
+ *        natural-log sum or NULL.  A token that sees no row gets out = 0 and
+ *        lse = -inf.  Tokens before q_start[0] and from q_start[B] on are
+ *        left as they are.
+ * A visible row weighs by its logit; a masked one weighs exactly 0 whatever
+ * it holds (NaN and infinities included).  A visible logit that is NaN or
+ * +inf makes its (token, head) row NaN, and no other.
+ * Precision: logits, sums and lse in fp32; the weights enter the value
+ * contraction rounded to bf16 (an output is within 2^-8 of the largest
+ * visible value magnitude before its own rounding).
+ * Faults: a q_start that is not ascending in [0, T], more than max_q tokens,
+ * a negative kv_len or rows outside [0, n_rows) set LS_FAULT_BAD_INDEX; rows
+ * outside the cache are not read and weigh nothing.
+ * Workspace: ls_window_attention_workspace_size() bytes (0 when the query rows
+ * alone fill the machine); calls that overlap on the GPU, replays of captured
+ * ones among them, need workspaces of their own.
+ */
+size_t ls_window_attention_workspace_size(int B, int T, int H, int max_q, int window, int align, int n_sink);
+ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
+                              const int32_t* kv_len, const int64_t* row_off, int B, int T, int H, int d, int d_v,
+                              int64_t n_rows, int max_q, int window, int align, int n_sink, float scale,
+                              int out_dtype, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ls_tree_attention -- attention of drafted tokens over their sequence's
+ * context and their own branch of the draft tree (the verification step of
+ * drafted decoding), over the same latent rows.
+ *
+ * Sequence b has the drafted tokens q_start[b] .. q_start[b+1] - 1 (n of
+ * them), the context rows 0 .. ctx_len[b] - 1 (from row_off[b]) and, behind
+ * them, the n drafted tokens' own rows.  Token t sees the context rows and
+ * drafted row i (i < n) exactly when bit i % 64 of tree_mask[t][i / 64] is
+ * set; a token's own bit is not implied.
+ * window > 0 cuts the context as in ls_window_attention, a token's position
+ * being ctx_len[b] + (drafted rows that it sees) - 1 (at least ctx_len[b]);
+ * drafted rows are never cut.  window = 0: the whole context.
+ *
+ *   tree_mask [T][words] 64-bit words, words >= ceil(max_q / 64)
+ *   max_ctx: the longest context, as far as the caller knows it (0: unknown);
+ *        it decides how the work is split, not what is computed, and the
+ *        workspace query has to be given the same
+ * Other arguments, outputs, faults and precision as ls_window_attention;
+ * ctx_len[b] + n rows have to lie in [0, n_rows).
+ */
+size_t ls_tree_attention_workspace_size(int B, int T, int H, int max_q, int64_t n_rows, int max_ctx, int window,
+                                        int align, int n_sink);
+ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
+                            const int32_t* ctx_len, const int64_t* row_off, const uint64_t* tree_mask, int words,
+                            int B, int T, int H, int d, int d_v, int64_t n_rows, int max_q, int max_ctx, int window,
+                            int align, int n_sink, float scale, int out_dtype, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * ls_norm_rope -- norm of the query heads and of the keys, the position
+ * rotation, and the write to their rows, in one pass: what stands between a
+ * layer's projections and ls_indexer_score* / the attentions ("03 long
+ * context", "The Architectural Answer: Read Less of the Past": the 132-byte
+ * indexer key is 128 fp8 codes and their scale).
+ *
+ * Each head row x of d elements becomes
+ *   y[i] = (x[i] - mu) * rsqrt(mean((x - mu)^2) + eps) * weight[i] + bias[i]
+ * for i < norm_dim (mean over those; LS_NORM_RMS: mu = 0; LS_NORM_NONE: y = x;
+ * elements from norm_dim on stay as they are), and then its elements rope_off
+ * .. rope_off + rope_dim - 1 are rotated in pairs (a, b) by f = pos[t] *
+ * inv_freq[i], a' = a cos f - b sin f, b' = b cos f + a sin f: pair i is
+ * (2i, 2i + 1) of that part (interleaved) or (i, i + rope_dim / 2).  The
+ * angles are formed in 64 bits.
+ *
+ * q and k (either may be NULL) describe the two kinds of rows:
+ *   x [T][heads][d] bf16, a token's rows x_stride elements apart (a multiple
+ *        of 8, >= heads * d: a part of a fused projection is read in place)
+ *   weight, bias [norm_dim] fp32 or NULL (ones, zeros), shared by the heads
+ *   out  [..][heads][d] bf16 or, out_dtype LS_KEY_FP8_E4M3, e4m3 codes with
+ *        scale [..][heads] fp32: scale = max |y| / 448 (1 for a row of
+ *        zeros), code = y / scale rounded to nearest even
+ *   slots [T] int64 or NULL: the output row of token t, for a cache of
+ *        out_rows rows; -1 writes nothing.  Other rows are left as they are;
+ *        a slot outside [-1, out_rows) writes nothing and sets
+ *        LS_FAULT_BAD_INDEX; of two tokens with one slot either may win.
+ *        NULL: row t.
+ * x and out must not overlap.  d a multiple of 8 up to 1024, norm_dim a
+ * multiple of 8 in [8, d] (0 without a norm), rope_dim even in [0, 256],
+ * rope_off + rope_dim <= d.  pos [T] int64, inv_freq [rope_dim / 2] fp32.
+ * x, out 16-byte aligned.  No workspace.
+ */
+#define LS_NORM_NONE 0
+#define LS_NORM_RMS 1
+#define LS_NORM_LAYER 2
+typedef struct ls_norm_rows {
+  const uint16_t* x;
+  int64_t x_stride;
+  int heads;
+  int norm; /* LS_NORM_* */
+  const float* weight;
+  const float* bias;
+  void* out;
+  float* scale;
+  const int64_t* slots;
+  int64_t out_rows;
+} ls_norm_rows;
+ls_status ls_norm_rope(const ls_norm_rows* q, const ls_norm_rows* k, const int64_t* pos, const float* inv_freq,
+                       int T, int d, int norm_dim, int rope_dim, int rope_off, int interleaved, float eps,
+                       int out_dtype, void* stream);
+
 /*
  * ls_decode_two_stage_select -- LeanSparse two-stage decode search
  * (podcast transcript, 07:12-08:00): scan compact keys, keep a shortlist,

@@ -74,3 +74,73 @@ def merge_partials(o_a: np.ndarray, lse_a: np.ndarray, o_b: np.ndarray, lse_b: n
         wa = np.where(np.isneginf(lse_a), 0.0, np.exp(lse_a - lse))
         wb = np.where(np.isneginf(lse_b), 0.0, np.exp(lse_b - lse))
     return wa[..., None] * o_a + wb[..., None] * o_b, lse
+
+
+def window_rows(p: int, window: int, align: int, n_sink: int) -> list[int]:
+    """Rows of its sequence that the token at position p sees: the sinks and
+    its window (the last `window` rows with its own, the start rounded down to
+    a multiple of `align`), none behind it."""
+    start = p - window + 1
+    if start > 0:
+        while start % align:
+            start -= 1
+    return [j for j in range(p + 1) if j < n_sink or j >= start]
+
+
+def window_attention(q, latent, q_start, kv_len, row_off, window, align, n_sink, scale, d_v: int = VALUE):
+    """q [T, H, D], latent [N, D] (float64) -> (o [T, H, d_v], lse [T, H]) of
+    every token that a sequence holds (the others: o = 0, lse = -inf)."""
+    seen = [[] for _ in range(q.shape[0])]
+    for b in range(len(kv_len)):
+        n = q_start[b + 1] - q_start[b]
+        for i in range(n):
+            seen[q_start[b] + i] = [row_off[b] + j for j in window_rows(kv_len[b] - n + i, window, align, n_sink)]
+    return rows_attention(q, latent, seen, scale, d_v)
+
+
+def tree_attention(q, latent, q_start, ctx_len, row_off, branches, window, align, n_sink, scale, d_v: int = VALUE):
+    """branches[t]: the drafted tokens (of its sequence) that token t sees.
+    The context is whole (window 0) or cut at the token's position, ctx_len +
+    the number of drafted tokens that it sees - 1."""
+    seen = [[] for _ in range(q.shape[0])]
+    for b in range(len(ctx_len)):
+        n = q_start[b + 1] - q_start[b]
+        for t in range(q_start[b], q_start[b + 1]):
+            mine = sorted(i for i in branches[t] if i < n)
+            ctx = range(ctx_len[b])
+            if window > 0:
+                near = set(window_rows(ctx_len[b] + max(0, len(mine) - 1), window, align, n_sink))
+                ctx = [j for j in ctx if j in near]
+            seen[t] = [row_off[b] + j for j in ctx] + [row_off[b] + ctx_len[b] + i for i in mine]
+    return rows_attention(q, latent, seen, scale, d_v)
+
+
+def rows_attention(q, latent, seen, scale, d_v: int = VALUE):
+    """Attention of token t over the latent rows seen[t]."""
+    o = np.zeros((q.shape[0], q.shape[1], d_v))
+    lse = np.full(q.shape[:2], -np.inf)
+    for t, rows in enumerate(seen):
+        if rows:
+            idx = np.asarray(rows, dtype=np.int64)[None, :]
+            o[t:t + 1], lse[t:t + 1] = sparse_attention(q[t:t + 1], latent, idx, scale, d_v)
+    return o, lse
+
+
+def norm_rope(x, pos, inv_freq, norm, norm_dim, weight, bias, eps, rope_off, interleaved):
+    """x [T, h, d] float64 -> the normed and rotated rows, float64 (element by
+    element: the definition, not a fast form)."""
+    y = np.array(x, dtype=np.float64)
+    if norm != "none":
+        a = y[..., :norm_dim]
+        if norm == "layer":
+            a = a - a.mean(axis=-1, keepdims=True)
+        a = a / np.sqrt((a * a).mean(axis=-1, keepdims=True) + eps)
+        y[..., :norm_dim] = a * (1.0 if weight is None else weight) + (0.0 if bias is None else bias)
+    half = len(inv_freq)
+    for i in range(half):
+        f = np.asarray(pos, dtype=np.float64) * np.float64(inv_freq[i])
+        c, s = np.cos(f)[:, None], np.sin(f)[:, None]
+        ia, ib = (rope_off + 2 * i, rope_off + 2 * i + 1) if interleaved else (rope_off + i, rope_off + half + i)
+        a, b = y[..., ia].copy(), y[..., ib].copy()
+        y[..., ia], y[..., ib] = a * c - b * s, b * c + a * s
+    return y

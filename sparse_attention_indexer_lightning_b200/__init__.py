@@ -26,6 +26,7 @@ from ._lib import (  # noqa: F401
     ls_lsa_tree_levels_workspace_size,
     ls_lsa_tree_select,
     ls_merge_select,
+    ls_norm_rope,
     ls_sparse_attention,
     ls_attention_merge,
     ls_prefill_select_stream,
@@ -34,6 +35,8 @@ from ._lib import (  # noqa: F401
     ls_profile_end,
     ls_selftest_wait_probe,
     ls_topk_select,
+    ls_tree_attention,
+    ls_window_attention,
     lib,
     shard_plan,
 )

@@ -32,6 +32,9 @@ LS_FAULT_WAIT_TIMEOUT = 1
 LS_FAULT_BAD_INDEX = 2
 LS_ATTN_FOREIGN_ROWS = 1
 LS_ATTN_CUDA_CORES = 2
+LS_OUT_F32 = 0
+LS_OUT_BF16 = 1
+LS_NORM = {"none": 0, "rms": 1, "layer": 2}
 
 EXPORTED = (
     "ls_last_error", "ls_version", "ls_device_status", "ls_indexer_score", "ls_topk_select",
@@ -43,9 +46,19 @@ EXPORTED = (
     "ls_prefill_select_fp8_workspace_size", "ls_prefill_select_stream_fp8", "ls_lsa_flat_workspace_size",
     "ls_lsa_flat_select", "ls_lsa_tree_workspace_size", "ls_lsa_tree_select", "ls_merge_select_workspace_size",
     "ls_merge_select", "ls_sparse_attention", "ls_attention_merge", "ls_lsa_tree_levels_workspace_size",
-    "ls_lsa_tree_levels_select",
+    "ls_lsa_tree_levels_select", "ls_window_attention_workspace_size", "ls_window_attention",
+    "ls_tree_attention_workspace_size", "ls_tree_attention", "ls_norm_rope",
 )
 HIST_BINS = 2048
+
+
+class NormRows(ctypes.Structure):
+    """ls_norm_rows of the C ABI: the rows of one operand of ls_norm_rope."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("heads", ctypes.c_int),
+                ("norm", ctypes.c_int), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("out_rows", ctypes.c_int64)]
 
 
 class LSError(RuntimeError):
@@ -97,6 +110,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ls_merge_select": (I, [P, P, P, I, I, I, I, P, P, P, SZ, P]),
         "ls_sparse_attention": (I, [P, P, P, P, I, I, I, I, I64, I, ctypes.c_float, I, P, P, P]),
         "ls_attention_merge": (I, [P, P, I, I64, I, P, P, P]),
+        "ls_window_attention_workspace_size": (SZ, [I, I, I, I, I, I, I]),
+        "ls_window_attention": (I, [P, P, P, P, P, I, I, I, I, I, I64, I, I, I, I, ctypes.c_float, I, P, P, P, SZ,
+                                    P]),
+        "ls_tree_attention_workspace_size": (SZ, [I, I, I, I, I64, I, I, I, I]),
+        "ls_tree_attention": (I, [P, P, P, P, P, P, I, I, I, I, I, I, I64, I, I, I, I, I, ctypes.c_float, I, P, P, P,
+                                  SZ, P]),
+        "ls_norm_rope": (I, [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, P]),
     }
     for name, (res, args) in sig.items():
         try:
@@ -641,6 +661,225 @@ def ls_attention_merge(o_parts, lse_parts, out=None, stream=None):
     _check(lib().ls_attention_merge(_ptr(o_parts), _ptr(lse_parts), S, rows, d_v, _ptr(o), _ptr(lse),
                                     _stream(stream)))
     return o, lse
+
+
+def _on(t: torch.Tensor, stream):
+    """Context in which a call's outputs and workspace are allocated and its kernels launched: t's device, and
+    `stream` (default: the device's current one), so that scratch memory belongs to the stream that uses it."""
+    if t.device.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if stream is None:
+        return torch.cuda.device(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _together(ref: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {ref.device}")
+
+
+def _span_args(q, latent, q_start, lens, row_off, max_q, scale, out_dtype, out, want_lse, lens_name):
+    """Checks and outputs that the two span attentions share -> (max_q, scale, out dtype code, out, lse)."""
+    _dev(q, torch.bfloat16, "q", 3)
+    _dev(latent, torch.bfloat16, "latent", 2)
+    _dev(q_start, torch.int32, "q_start", 1)
+    _dev(lens, torch.int32, lens_name, 1)
+    _opt(row_off, torch.int64, "row_off")
+    T, H, d = q.shape
+    B = lens.shape[0]
+    if latent.shape[1] != d:
+        raise ValueError(f"q has {d} elements per head, latent rows {latent.shape[1]}")
+    if q_start.shape[0] != B + 1:
+        raise ValueError(f"q_start has {q_start.shape[0]} entries for {B} sequences")
+    if row_off is not None and tuple(row_off.shape) != (B,):
+        raise ValueError(f"row_off has shape {tuple(row_off.shape)} for {B} sequences")
+    _together(q, latent=latent, q_start=q_start, row_off=row_off, **{lens_name: lens})
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+    max_q = T if max_q is None else int(max_q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.empty((T, H, 512), dtype=out_dtype, device=q.device)
+    else:
+        _dev(out, out_dtype, "out", 3)
+        _together(q, out=out)
+        if tuple(out.shape) != (T, H, 512):
+            raise ValueError(f"out has shape {tuple(out.shape)}, not {(T, H, 512)}")
+    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_lse else None
+    return max_q, float(scale), LS_OUT_BF16 if out_dtype == torch.bfloat16 else LS_OUT_F32, out, lse
+
+
+def _span_ws(ws, need, q):
+    if ws is None:
+        return _workspace(need, q.device)
+    _dev(ws, torch.uint8, "ws", 1)
+    _together(q, ws=ws)
+    return ws
+
+
+def ls_window_attention(q, latent, q_start, kv_len, row_off=None, window: int = 512, align: int = 1,
+                        n_sink: int = 4, max_q: Optional[int] = None, scale: Optional[float] = None,
+                        out_dtype=torch.bfloat16, want_lse: bool = True, ws=None, out=None, stream=None):
+    """Attention over the sinks and the window of each sequence's latent rows.
+
+    q [T,H,576] bf16, the tokens of sequence b at q_start[b] .. q_start[b+1]-1; latent [R,576] bf16; q_start [B+1]
+    and kv_len [B] int32, row_off [B] int64 or None: the sequence's kv_len rows (its query tokens' own ones last)
+    start at row row_off.  The token at position p sees row j <= p when j < n_sink or j >= lo, lo = max(0,
+    p - window + 1) rounded down to a multiple of align (window=1, align=512: the block window of the LSA search).
+    max_q: at least the longest sequence's query tokens (default T) -> (out [T,H,512] of out_dtype, lse [T,H] f32 or
+    None); out_dtype=torch.float32 is what ls_attention_merge joins with other parts."""
+    with _on(q, stream):
+        max_q, scale, od, out, lse = _span_args(q, latent, q_start, kv_len, row_off, max_q, scale, out_dtype, out,
+                                                want_lse, "kv_len")
+        T, H, d = q.shape
+        B = kv_len.shape[0]
+        ws = _span_ws(ws, lib().ls_window_attention_workspace_size(B, T, H, max_q, window, align, n_sink), q)
+        _check(lib().ls_window_attention(_ptr(q), _ptr(latent), _ptr(q_start), _ptr(kv_len), _ptr(row_off), B, T, H,
+                                         d, 512, latent.shape[0], max_q, window, align, n_sink, scale, od,
+                                         _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream()))
+    return out, lse
+
+
+def ls_tree_attention(q, latent, q_start, ctx_len, tree_mask, row_off=None, window: int = 0, align: int = 1,
+                      n_sink: int = 0, max_q: Optional[int] = None, max_ctx: int = 0,
+                      scale: Optional[float] = None, out_dtype=torch.bfloat16, want_lse: bool = True, ws=None,
+                      out=None, stream=None):
+    """Attention of drafted tokens over their context and their branch of the draft tree.
+
+    q [T,H,576] bf16 and q_start as in ls_window_attention; sequence b's ctx_len[b] context rows start at row
+    row_off[b], its drafted tokens' own rows follow them.  tree_mask [T,words] int64: bit i % 64 of word i // 64 of
+    token t is set when it sees drafted row i of its sequence (its own included).  window > 0 cuts the context as in
+    ls_window_attention.  max_ctx: the longest context if the caller knows it (it only decides how the work is
+    split) -> (out [T,H,512] of out_dtype, lse [T,H] f32 or None)."""
+    with _on(q, stream):
+        max_q, scale, od, out, lse = _span_args(q, latent, q_start, ctx_len, row_off, max_q, scale, out_dtype, out,
+                                                want_lse, "ctx_len")
+        T, H, d = q.shape
+        B, R = ctx_len.shape[0], latent.shape[0]
+        _dev(tree_mask, torch.int64, "tree_mask", 2)
+        _together(q, tree_mask=tree_mask)
+        if tree_mask.shape[0] != T:
+            raise ValueError(f"tree_mask has {tree_mask.shape[0]} rows for {T} tokens")
+        ws = _span_ws(ws, lib().ls_tree_attention_workspace_size(B, T, H, max_q, R, max_ctx, window, align, n_sink),
+                      q)
+        _check(lib().ls_tree_attention(_ptr(q), _ptr(latent), _ptr(q_start), _ptr(ctx_len), _ptr(row_off),
+                                       _ptr(tree_mask), tree_mask.shape[1], B, T, H, d, 512, R, max_q, max_ctx,
+                                       window, align, n_sink, scale, od, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                       _stream()))
+    return out, lse
+
+
+def _norm_rows(x, name, norm, norm_dim, weight, bias, out, scale, slots):
+    if norm not in LS_NORM:
+        raise ValueError(f"{name}_norm must be one of {sorted(LS_NORM)}, got {norm!r}")
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _dev(t, torch.float32, f"{name}_{what}", 1)
+            if t.shape[0] != norm_dim:
+                raise ValueError(f"{name}_{what} has {t.shape[0]} elements for norm_dim = {norm_dim}")
+            if norm == "none":
+                raise ValueError(f"{name}_{what} without a norm")
+    T, H, d = x.shape
+    p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    return NormRows(p(x), max(x.stride(0), H * d) if T <= 1 else x.stride(0), H, LS_NORM[norm], p(weight), p(bias),
+                    p(out), p(scale), p(slots), 0 if slots is None else out.shape[0])
+
+
+def _head_rows(x, name):
+    """x [T,heads,d] bf16 whose heads lie side by side; a token's rows may be part of a longer row."""
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(x.shape)}")
+    T, H, d = x.shape
+    if x.numel() and (x.stride(2) != 1 and d > 1 or (x.stride(1) != d and H > 1) or (T > 1 and x.stride(0) < H * d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {x.stride()})")
+    return x
+
+
+def ls_norm_rope(q=None, k=None, pos=None, inv_freq=None, q_norm: str = "none", k_norm: str = "none",
+                 norm_dim: Optional[int] = None, q_weight=None, q_bias=None, k_weight=None, k_bias=None,
+                 eps: float = 1e-6, rope_off: int = 0, interleaved: bool = False, fp8: Optional[bool] = None,
+                 k_cache=None, k_scale=None, slots=None, stream=None):
+    """Norm, position rotation and the write of query heads and keys, in one pass over each.
+
+    q [T,Hq,d] and k [T,Hk,d] bf16 (either may be None; a token's heads contiguous, so slices of a fused projection
+    are read in place); *_norm "none" | "rms" | "layer" over the first norm_dim elements (default d) with weights and
+    biases [norm_dim] f32; pos [T] int64 and inv_freq [rope/2] f32 rotate the elements from rope_off on, in pairs
+    (2i, 2i+1) when interleaved, else (i, i + rope/2); inv_freq None: no rotation.
+    k_cache [R,Hk,d] or, Hk = 1, [R,d] (bf16 or float8_e4m3fn) with slots [T] int64 takes the keys at rows slots[t]
+    (-1: nowhere), k_scale [R,Hk] or [R] f32 the scales of an fp8 cache.  fp8 (default: k_cache's type, else False)
+    asks for codes and scales.  -> (q_out [T,Hq,d], q_scale [T,Hq] or None, k_out, k_scale or None); k_out is k_cache
+    when that is given."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("ls_norm_rope needs q or k")
+    with _on(x, stream):
+        for t, name in ((q, "q"), (k, "k")):
+            if t is not None:
+                _head_rows(t, name)
+        T, _, d = x.shape
+        if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d):
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree")
+        norm_dim = d if norm_dim is None else int(norm_dim)
+        rope = 0
+        if inv_freq is not None:
+            _dev(inv_freq, torch.float32, "inv_freq", 1)
+            rope = 2 * inv_freq.shape[0]
+            if pos is None:
+                raise ValueError("inv_freq without pos")
+            _dev(pos, torch.int64, "pos", 1)
+            if pos.shape[0] != T:
+                raise ValueError(f"pos has {pos.shape[0]} entries for {T} tokens")
+        if fp8 is None:
+            fp8 = k_cache is not None and k_cache.dtype == torch.float8_e4m3fn
+        dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+        _together(x, q=q, k=k, pos=pos, inv_freq=inv_freq, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight,
+                  k_bias=k_bias, k_cache=k_cache, k_scale=k_scale, slots=slots)
+        if k_cache is None:
+            if slots is not None or k_scale is not None:
+                raise ValueError("slots and k_scale belong to k_cache")
+        else:
+            if k is None:
+                raise ValueError("k_cache without k")
+            if slots is None:
+                raise ValueError("k_cache needs slots")
+            _dev(slots, torch.int64, "slots", 1)
+            if slots.shape[0] != T:
+                raise ValueError(f"slots has {slots.shape[0]} entries for {T} tokens")
+            _dev(k_cache, dt, "k_cache")
+            if tuple(k_cache.shape[1:]) not in ((k.shape[1], d), (d,) if k.shape[1] == 1 else None):
+                raise ValueError(f"k_cache {tuple(k_cache.shape)} does not hold rows of k {tuple(k.shape)}")
+            if fp8:
+                if k_scale is None:
+                    raise ValueError("an fp8 k_cache needs k_scale")
+                _dev(k_scale, torch.float32, "k_scale")
+                if k_scale.numel() != k_cache.shape[0] * k.shape[1]:
+                    raise ValueError(f"k_scale {tuple(k_scale.shape)} does not belong to {tuple(k_cache.shape)}")
+            elif k_scale is not None:
+                raise ValueError("k_scale with a bf16 k_cache")
+        q_out = q_scale = k_out = None
+        rows = [None, None]
+        if q is not None:
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+            q_scale = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if fp8 else None
+            rows[0] = _norm_rows(q, "q", q_norm, norm_dim, q_weight, q_bias, q_out, q_scale, None)
+        if k is not None:
+            k_out = k_cache
+            if k_cache is None:
+                k_out = torch.empty(k.shape, dtype=dt, device=k.device)
+                k_scale = torch.empty(k.shape[:2], dtype=torch.float32, device=k.device) if fp8 else None
+            rows[1] = _norm_rows(k, "k", k_norm, norm_dim, k_weight, k_bias, k_out, k_scale, slots)
+        _check(lib().ls_norm_rope(*(None if r is None else ctypes.byref(r) for r in rows), _ptr(pos),
+                                  _ptr(inv_freq), T, d, norm_dim, rope, rope_off, int(interleaved), float(eps),
+                                  LS_KEY_FP8_E4M3 if fp8 else LS_KEY_BF16, _stream()))
+    return q_out, q_scale, k_out, k_scale
 
 
 def shard_plan(n_keys: int, n_shards: int):

@@ -21,7 +21,9 @@
 #include "score_cvt.cuh"
 #include "score_dot.cuh"
 #include "score_tree.cuh"
+#include "latent_attn.cuh"
 #include "merge.cuh"
+#include "norm_rope.cuh"
 #include "sparse_attn.cuh"
 #include "sparse_attn_tc.cuh"
 #include "score_q8.cuh"
@@ -1617,6 +1619,227 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof("attn_merge_kernel", st);
   LS_CUDA(launch_attn_merge(o_parts, lse_parts, S, rows, d_v, o, lse, num_sms_current(), st));
+  return LS_OK;
+}
+
+namespace {
+
+// Tiles of the cache that one tile of query rows can meet, at most.
+int64_t span_tiles(int H, int max_q, int64_t ctx, int window, int align, int n_sink, int drafted) {
+  int64_t span = ctx;                                 // the whole context
+  int64_t sinks = 0;
+  if (window > 0) {
+    const int64_t toks = std::min<int64_t>(max_q, (kLaRows - 1) / H + 2);   // tokens of a query tile
+    const int64_t w = static_cast<int64_t>(window) + align - 1 + toks - 1;
+    if (ctx <= 0 || w < ctx) {
+      span = w;
+      sinks = (n_sink + kLaTile - 1) / kLaTile;
+    }
+  }
+  return sinks + (span + kLaTile - 1) / kLaTile + (drafted + kLaTile - 1) / kLaTile;
+}
+
+int query_tiles(int H, int max_q) {
+  return static_cast<int>((static_cast<int64_t>(max_q) * H + kLaRows - 1) / kLaRows);
+}
+
+size_t span_workspace(int T, int H, int n_split) {
+  if (n_split <= 1) return 0;
+  const size_t rows = static_cast<size_t>(n_split) * T * H;
+  return align_up(rows * kAttnValue * sizeof(float)) + align_up(rows * sizeof(float));
+}
+
+bool span_sizes_ok(int B, int T, int H, int max_q, int window, int align, int n_sink, bool tree) {
+  return B >= 0 && T >= 0 && H >= 1 && H <= 1024 && max_q >= 0 && static_cast<int64_t>(T) * H <= 0x7fffffffLL &&
+         window >= (tree ? 0 : 1) && align >= 1 && n_sink >= 0 &&
+         static_cast<int64_t>(window) + align <= (1 << 30);
+}
+
+int window_splits(int B, int H, int max_q, int window, int align, int n_sink) {
+  return la_splits(static_cast<int64_t>(B) * query_tiles(H, max_q),
+                   span_tiles(H, max_q, 0, window, align, n_sink, 0));
+}
+
+int tree_splits(int B, int H, int max_q, int64_t n_rows, int max_ctx, int window, int align, int n_sink) {
+  const int64_t ctx = max_ctx > 0 && max_ctx < n_rows ? max_ctx : n_rows;
+  return la_splits(static_cast<int64_t>(B) * query_tiles(H, max_q),
+                   span_tiles(H, max_q, ctx, window, align, n_sink, max_q));
+}
+
+// Shared checks, tensor maps and launches of the two span attentions.
+ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* latent, int max_q, int out_dtype,
+                         void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (d != kAttnLatent || d_v != kAttnValue)
+    return fail(LS_ERR_UNSUPPORTED, "latent rows of %d elements with %d value elements are built (got d=%d d_v=%d)",
+                kAttnLatent, kAttnValue, d, d_v);
+  LS_CHECK_ARG(out_dtype == LS_OUT_F32 || out_dtype == LS_OUT_BF16, "unknown out_dtype %d", out_dtype);
+  LS_CHECK_ARG(p.scale == p.scale && p.scale > -3.4e38f && p.scale < 3.4e38f, "scale must be finite");
+  LS_CHECK_ARG(p.n_rows >= 1 && p.n_rows + p.T <= 0x7fffffffLL, "n_rows must be in [1, 2^31 - 1 - T] (got %lld)",
+               static_cast<long long>(p.n_rows));
+  if (p.B == 0 || p.T == 0 || max_q == 0) return LS_OK;
+  LS_CHECK_ARG(p.q && latent && p.q_start && p.kv_len && p.out, "null tensor pointer");
+  LS_CHECK_ARG(aligned16(p.q) && aligned16(latent) && aligned16(p.out), "q, latent and out must be 16-byte aligned");
+  p.max_tiles = query_tiles(p.H, max_q);
+  LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles * p.n_split * 2 <= 0x7fffffffLL, "B * max_q * H too large");
+  p.out_bf16 = out_dtype == LS_OUT_BF16;
+  const size_t need = span_workspace(p.T, p.H, p.n_split);
+  if (need > 0) {
+    if (ws_bytes < need) return fail(LS_ERR_WORKSPACE, "workspace of %zu B, %zu B needed", ws_bytes, need);
+    LS_CHECK_ARG(ws && aligned16(ws), "the workspace must be a 16-byte aligned device pointer");
+    Carver c(ws);
+    p.part_o = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H * kAttnValue);
+    p.part_lse = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H);
+  }
+  CUtensorMap qmap, map64, map16;
+  ls_status s = make_latent_map(&qmap, p.q, static_cast<uint64_t>(p.T) * p.H, kLaRows);
+  if (s == LS_OK) s = make_latent_map(&map64, latent, static_cast<uint64_t>(p.n_rows), kLaTile);
+  if (s == LS_OK) s = make_latent_map(&map16, latent, static_cast<uint64_t>(p.n_rows), 16);
+  if (s != LS_OK) return s;
+  {
+    ProfScope prof("latent_attn_kernel", st);
+    LS_CUDA(launch_latent_attn(&qmap, &map64, &map16, p, st));
+  }
+  if (p.n_split > 1) {
+    ProfScope prof("latent_attn_combine_kernel", st);
+    LS_CUDA(launch_latent_attn_combine(p, st));
+  }
+  return LS_OK;
+}
+
+}  // namespace
+
+size_t ls_window_attention_workspace_size(int B, int T, int H, int max_q, int window, int align, int n_sink) {
+  if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, false) || B == 0 || T == 0 || max_q == 0) return 0;
+  return span_workspace(T, H, window_splits(B, H, std::min(max_q, T), window, align, n_sink));
+}
+
+ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
+                              const int32_t* kv_len, const int64_t* row_off, int B, int T, int H, int d, int d_v,
+                              int64_t n_rows, int max_q, int window, int align, int n_sink, float scale,
+                              int out_dtype, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  LS_CHECK_ARG(span_sizes_ok(B, T, H, max_q, window, align, n_sink, false),
+               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: H in [1, 1024], T * H < 2^31, "
+               "window and align >= 1, window + align <= 2^30)",
+               B, T, H, max_q, window, align, n_sink);
+  max_q = std::min(max_q, T);
+  LatentAttnParams p;
+  p.q = q;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.row_off = row_off;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.n_rows = n_rows;
+  p.window = window;
+  p.align = align;
+  p.n_sink = n_sink;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  if (B > 0 && max_q > 0) p.n_split = window_splits(B, H, max_q, window, align, n_sink);
+  return span_attention(p, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
+}
+
+size_t ls_tree_attention_workspace_size(int B, int T, int H, int max_q, int64_t n_rows, int max_ctx, int window,
+                                        int align, int n_sink) {
+  if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, true) || n_rows < 1 || B == 0 || T == 0 || max_q == 0)
+    return 0;
+  return span_workspace(T, H, tree_splits(B, H, std::min(max_q, T), n_rows, max_ctx, window, align, n_sink));
+}
+
+ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
+                            const int32_t* ctx_len, const int64_t* row_off, const uint64_t* tree_mask, int words,
+                            int B, int T, int H, int d, int d_v, int64_t n_rows, int max_q, int max_ctx, int window,
+                            int align, int n_sink, float scale, int out_dtype, void* out, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  LS_CHECK_ARG(span_sizes_ok(B, T, H, max_q, window, align, n_sink, true),
+               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: H in [1, 1024], T * H < 2^31, "
+               "window >= 0, align >= 1, window + align <= 2^30)",
+               B, T, H, max_q, window, align, n_sink);
+  max_q = std::min(max_q, T);
+  LS_CHECK_ARG(words >= (max_q + 63) / 64, "tree_mask has %d words a token for max_q = %d", words, max_q);
+  LS_CHECK_ARG(tree_mask || T == 0 || B == 0, "null tree_mask");
+  LatentAttnParams p;
+  p.q = q;
+  p.q_start = q_start;
+  p.kv_len = ctx_len;
+  p.row_off = row_off;
+  p.tree = tree_mask;
+  p.words = words;
+  p.B = B;
+  p.T = T;
+  p.H = H;
+  p.n_rows = n_rows;
+  p.window = window;
+  p.align = align;
+  p.n_sink = n_sink;
+  p.scale = scale;
+  p.out = out;
+  p.lse = lse;
+  if (B > 0 && max_q > 0 && n_rows >= 1)
+    p.n_split = tree_splits(B, H, max_q, n_rows, max_ctx, window, align, n_sink);
+  return span_attention(p, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
+}
+
+ls_status ls_norm_rope(const ls_norm_rows* q, const ls_norm_rows* k, const int64_t* pos, const float* inv_freq,
+                       int T, int d, int norm_dim, int rope_dim, int rope_off, int interleaved, float eps,
+                       int out_dtype, void* stream) {
+  LS_CHECK_ARG(T >= 0, "negative T");
+  LS_CHECK_ARG(d >= 8 && d % 8 == 0 && d <= kNrMaxDim, "d must be a multiple of 8 in [8, %d] (got %d)", kNrMaxDim, d);
+  LS_CHECK_ARG(rope_dim >= 0 && rope_dim % 2 == 0 && rope_dim <= kNrMaxRope && rope_off >= 0 &&
+                   rope_off <= d - rope_dim,
+               "rope_dim must be even in [0, %d] and inside the row (rope_off=%d rope_dim=%d d=%d)", kNrMaxRope,
+               rope_off, rope_dim, d);
+  LS_CHECK_ARG(eps >= 0.f && eps < 3.4e38f, "eps must be finite and not negative");
+  LS_CHECK_ARG(out_dtype == LS_KEY_BF16 || out_dtype == LS_KEY_FP8_E4M3, "unknown out_dtype %d", out_dtype);
+  NormRopeParams p;
+  const ls_norm_rows* in[2] = {q, k};
+  const char* names[2] = {"q", "k"};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    const ls_norm_rows& r = *in[i];
+    LS_CHECK_ARG(r.heads >= 1 && r.heads <= 4096, "%s: heads must be in [1, 4096] (got %d)", names[i], r.heads);
+    LS_CHECK_ARG(r.norm == LS_NORM_NONE || r.norm == LS_NORM_RMS || r.norm == LS_NORM_LAYER, "%s: unknown norm %d",
+                 names[i], r.norm);
+    LS_CHECK_ARG(r.norm == LS_NORM_NONE || (norm_dim >= 8 && norm_dim % 8 == 0 && norm_dim <= d),
+                 "norm_dim must be a multiple of 8 in [8, d] (got %d)", norm_dim);
+    LS_CHECK_ARG(r.x_stride % 8 == 0 && r.x_stride >= static_cast<int64_t>(r.heads) * d,
+                 "%s: x_stride must be a multiple of 8 and at least heads * d (got %lld)", names[i],
+                 static_cast<long long>(r.x_stride));
+    LS_CHECK_ARG(r.slots == nullptr || r.out_rows >= 0, "%s: negative out_rows", names[i]);
+    if (T > 0) {
+      LS_CHECK_ARG(r.x && r.out, "%s: null tensor pointer", names[i]);
+      LS_CHECK_ARG(aligned16(r.x) && aligned16(r.out), "%s: x and out must be 16-byte aligned", names[i]);
+      LS_CHECK_ARG(out_dtype == LS_KEY_BF16 || r.scale, "%s: fp8 rows need a scale output", names[i]);
+    }
+    NormRows& o = p.part[i];
+    o.x = r.x;
+    o.x_stride = r.x_stride;
+    o.heads = r.heads;
+    o.norm = r.norm;
+    o.weight = r.weight;
+    o.bias = r.bias;
+    o.out = r.out;
+    o.scale = r.scale;
+    o.slots = r.slots;
+    o.out_rows = r.out_rows;
+  }
+  if (T == 0 || (!q && !k)) return LS_OK;
+  LS_CHECK_ARG(rope_dim == 0 || (pos && inv_freq), "null pos or inv_freq");
+  LS_CHECK_ARG(static_cast<int64_t>(T) * (p.part[0].heads + p.part[1].heads) <= 0x7fffffffLL, "T * heads too large");
+  p.pos = pos;
+  p.inv_freq = inv_freq;
+  p.T = T;
+  p.d = d;
+  p.norm_dim = norm_dim;
+  p.rope = rope_dim;
+  p.rope_off = rope_off;
+  p.interleaved = interleaved != 0;
+  p.fp8 = out_dtype == LS_KEY_FP8_E4M3;
+  p.eps = eps;
+  ProfScope prof("norm_rope_kernel", S(stream));
+  LS_CUDA(launch_norm_rope(p, num_sms_current(), S(stream)));
   return LS_OK;
 }
 

@@ -1,0 +1,635 @@
+// Attention of query tokens over whole spans of the latent cache on the
+// tensor cores (tcgen05): the window form (the first n_sink rows of a sequence
+// plus a sliding or block-aligned window of the latest ones; the sinks and the
+// window of "Latent Sparse Attention", "The method, term by term", step 6) and
+// the tree form (a context and, behind it, drafted rows of which a token sees
+// its own branch).  A latent row is 576 bf16 elements, the key of every head;
+// its first 512 are the value (absorbed MLA, as in sparse_attn.cuh):
+//
+//   z(s) = scale * q . c[s],  lse = log sum_s exp z(s),  o = sum_s exp(z(s) - lse) c[s, :512]
+//
+// The query heads of a sequence's tokens are consecutive rows of q, so 128 of
+// them (whatever the number of heads) are the M of every MMA.  One pass over
+// the rows any of them sees, in tiles of 64, with the running maximum and sum
+// of the softmax:
+//
+//  - tensor memory holds 512 columns, and an fp32 output of 512 value columns
+//    would take all of them; a CTA therefore keeps half of the value columns
+//    (256) and two CTAs work on the same 128 query rows, each computing the
+//    logits;
+//  - of the query's nine 64-element panels four live in tensor memory as the
+//    MMAs' A operand and five in shared memory (80 KB); two tiles of the cache
+//    (2 x 72 KB) are in flight beside them.  A tile is staged once: its four
+//    value panels are read as K-major keys by the logits and as MN-major
+//    values by the output (the same bytes);
+//  - the logits of tile i + 1 are issued before the output of tile i, so the
+//    softmax of a tile runs beside the MMAs of the next;
+//  - the weights go back to tensor memory as bf16 (A operand of the output);
+//    the output is rescaled only when a row's maximum grew by more than 8
+//    (in log2 units: weights stay below 2^8, so nothing overflows).
+//
+// Rounding to fewer bits: the weights (bf16, half a step is 2^-8 of a weight; the sum that
+// divides the output is that of the rounded weights, so they still sum to 1)
+// and the output when it is asked for in bf16.  Logits, sums, lse are fp32.
+//
+// Masked places weigh exactly 0 whatever they hold: a tile that not every row
+// sees whole is checked for logits that are not finite at masked places, and
+// only then the staged values are searched for elements that are not finite
+// (a weight of 0 times one of them would be NaN) and cleared.  A visible row
+// with a NaN or +inf logit makes its own query row NaN, and no other.
+//
+// Few query rows over a long span: the tiles are split over n_split CTA pairs,
+// each writing its part (fp32, with its lse) to the workspace, and
+// latent_attn_combine_kernel joins the parts.
+
+#pragma once
+
+#include "common.cuh"
+#include "sparse_attn.cuh"
+
+namespace lsi {
+
+constexpr int kLaRows = 128;                          // query rows per CTA: the MMA's M
+constexpr int kLaTile = 64;                           // cache rows per tile
+constexpr int kLaPanelBytes = kLaTile * 128;          // 8 KB: 64 elements of 64 rows
+constexpr int kLaVPanels = 4;                         // value panels of a CTA's half
+constexpr int kLaTPanels = 5;                         // panels only the logits read
+constexpr int kLaQTmem = 4;                           // query panels in tensor memory
+constexpr int kLaQSmem = 5;                           // query panels in shared memory
+constexpr int kLaQPanelBytes = kLaRows * 128;         // 16 KB
+constexpr int kLaBuf = (kLaVPanels + kLaTPanels) * kLaPanelBytes;   // 72 KB
+constexpr int kLaThreads = 6 * 32;                    // copies, MMA, 4 softmax / epilogue warps
+constexpr int kLaColO = 0, kLaColS = 256, kLaColQ = 384;            // tensor-memory columns
+constexpr float kLaLazy = 8.f;                        // log2 growth of a maximum that forces a rescale
+constexpr int kLaMaxSplit = 64;
+
+struct LaBars {
+  uint64_t qfull, qtmem;
+  uint64_t full_t[2], full_v[2];     // logit-only panels / value panels of a buffer have landed
+  uint64_t empty_t[2], empty_v[2];
+  uint64_t sfull[2];                 // logits in tensor memory
+  uint64_t pfull[2];                 // weights in tensor memory
+  uint64_t odone;                    // output MMAs of a tile are complete
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kLaOffBuf = size_t(kLaQSmem) * kLaQPanelBytes;
+constexpr size_t kLaOffBars = kLaOffBuf + 2 * size_t(kLaBuf);
+constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
+static_assert(sizeof(LaBars) <= 256, "barrier block");
+static_assert(kLaSmem <= 232448, "shared memory budget");
+
+struct LatentAttnParams {
+  const uint16_t* q = nullptr;        // [T * H][576]
+  const int32_t* q_start = nullptr;   // [B + 1]
+  const int32_t* kv_len = nullptr;    // [B]: window: rows with the tokens' own; tree: context rows
+  const int64_t* row_off = nullptr;   // [B] or nullptr (0)
+  const uint64_t* tree = nullptr;     // [T][words] or nullptr: the window form
+  int words = 0;
+  int B = 0, T = 0, H = 0;
+  int max_tiles = 0;                  // 128-row tiles per sequence that the grid covers
+  int64_t n_rows = 0;
+  int window = 0, align = 1, n_sink = 0;   // window <= 0 (tree only): the whole context
+  float scale = 0.f;
+  int n_split = 1;
+  int out_bf16 = 0;
+  void* out = nullptr;                // [T * H][512]
+  float* lse = nullptr;               // [T * H] or nullptr
+  float* part_o = nullptr;            // [n_split][T * H][512]
+  float* part_lse = nullptr;          // [n_split][T * H]
+};
+
+// First row of the window of the token at position p.
+__host__ __device__ inline int la_window_lo(int p, int window, int align) {
+  if (window <= 0) return 0;
+  const int x = p - window + 1;
+  return x <= 0 ? 0 : x - x % align;
+}
+
+__device__ __forceinline__ uint64_t la_low_mask(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
+// The rows that a tile of query rows can see, cut into tiles of 64.
+struct LaSpan {
+  int sink_len;          // rows [0, sink_len): sinks apart from the window
+  int lo, hi;            // window / context rows
+  int drafted;           // drafted rows behind the context
+  int n0, n1, n2;        // tiles of each
+  int lo_max, hi_min;    // rows [lo_max, hi_min) are in every query row's window
+  __device__ __forceinline__ int tiles() const { return n0 + n1 + n2; }
+  // kind 0: rows a .. a + cnt of the sequence; 1: drafted rows a .. a + cnt
+  __device__ __forceinline__ void tile(int i, int& kind, int& a, int& cnt) const {
+    if (i < n0) {
+      kind = 0;
+      a = kLaTile * i;
+      cnt = sink_len - a;
+    } else if (i < n0 + n1) {
+      kind = 0;
+      a = lo + kLaTile * (i - n0);
+      cnt = hi - a;
+    } else {
+      kind = 1;
+      a = kLaTile * (i - n0 - n1);
+      cnt = drafted - a;
+    }
+    cnt = cnt < kLaTile ? cnt : kLaTile;
+  }
+};
+
+// grid: B * max_tiles * n_split * 2 CTAs, the value half innermost.
+// qmap: q rows, box 64 x 128; map64 / map16: latent rows, boxes 64 x 64 and 64 x 16; 128-byte swizzle.
+__global__ void __launch_bounds__(kLaThreads, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map64,
+                       const __grid_constant__ CUtensorMap map16, const __grid_constant__ LatentAttnParams P) {
+  extern __shared__ uint8_t la_raw[];
+  uint8_t* smem = smem_align1024(la_raw);
+  LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ------------------------------------------------------------ this CTA's work
+  int64_t bid = blockIdx.x;
+  const int vh = static_cast<int>(bid & 1);
+  bid >>= 1;
+  const int split = static_cast<int>(bid % P.n_split);
+  bid /= P.n_split;
+  const int qtile = static_cast<int>(bid % P.max_tiles);
+  const int b = static_cast<int>(bid / P.max_tiles);
+  const int H = P.H;
+  const int t0 = __ldg(P.q_start + b), t1 = __ldg(P.q_start + b + 1);
+  if (t0 < 0 || t1 < t0 || t1 > P.T) {                // not a prefix of the tokens: nothing of it is computed
+    if (threadIdx.x == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
+    return;
+  }
+  const int n = t1 - t0;
+  const int64_t seq_rows = static_cast<int64_t>(n) * H;
+  if (seq_rows > static_cast<int64_t>(P.max_tiles) * kLaRows && threadIdx.x == 0)
+    atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: the rest is not computed
+  const int64_t r0 = static_cast<int64_t>(qtile) * kLaRows;
+  if (r0 >= seq_rows) return;
+  const int nrows = static_cast<int>(seq_rows - r0 < kLaRows ? seq_rows - r0 : kLaRows);
+  const int64_t grow0 = static_cast<int64_t>(t0) * H + r0;          // first row in q / out
+  const int tok_first = static_cast<int>(r0 / H), tok_last = static_cast<int>((r0 + nrows - 1) / H);
+  const bool is_tree = P.tree != nullptr;
+  int kv = __ldg(P.kv_len + b);
+  const int64_t off = P.row_off ? __ldg(P.row_off + b) : 0;
+  const int own = is_tree ? n : 0;                    // drafted rows behind kv
+  if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && threadIdx.x == 0)
+    atomicOr(&g_fault, FAULT_BAD_INDEX);              // rows outside the cache are not seen
+  kv = kv < 0 ? 0 : kv > P.n_rows ? static_cast<int>(P.n_rows) : kv;
+  int avail = 0;                                      // rows of the sequence that the cache holds
+  if (off >= 0 && off < P.n_rows)
+    avail = static_cast<int>(P.n_rows - off < kv + static_cast<int64_t>(own) ? P.n_rows - off : kv + own);
+  LaSpan sp;
+  if (is_tree) {
+    const int ctx = kv < avail ? kv : avail;
+    sp.drafted = avail - ctx;
+    sp.hi = sp.hi_min = ctx;
+    sp.lo = la_window_lo(kv, P.window, P.align);      // a token's depth is 0 at least, n - 1 at most
+    sp.lo_max = la_window_lo(kv + n - 1, P.window, P.align);
+  } else {
+    const int p0 = kv - n + tok_first, p1 = kv - n + tok_last;
+    sp.drafted = 0;
+    sp.hi = p1 + 1 < avail ? p1 + 1 : avail;
+    sp.hi_min = p0 + 1 < avail ? p0 + 1 : avail;
+    sp.lo = la_window_lo(p0, P.window, P.align);
+    sp.lo_max = la_window_lo(p1, P.window, P.align);
+  }
+  if (sp.hi < 0) sp.hi = 0;
+  sp.sink_len = P.n_sink < sp.hi ? P.n_sink : sp.hi;
+  if (sp.lo <= sp.sink_len) {
+    sp.lo = 0;
+    sp.sink_len = 0;
+  }
+  sp.n0 = (sp.sink_len + kLaTile - 1) / kLaTile;
+  sp.n1 = sp.hi > sp.lo ? (sp.hi - sp.lo + kLaTile - 1) / kLaTile : 0;
+  sp.n2 = (sp.drafted + kLaTile - 1) / kLaTile;
+  const int all = sp.tiles();
+  const int per = (all + P.n_split - 1) / P.n_split;
+  const int i0 = split * per < all ? split * per : all;
+  const int i1 = i0 + per < all ? i0 + per : all;
+  const int nt = i1 - i0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->qfull, 1);
+    mbar_init(&bars->qtmem, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->full_t[i], 1);
+      mbar_init(&bars->full_v[i], 1);
+      mbar_init(&bars->empty_t[i], 1);
+      mbar_init(&bars->empty_v[i], 1);
+      mbar_init(&bars->sfull[i], 1);
+      mbar_init(&bars->pfull[i], 4);
+    }
+    mbar_init(&bars->odone, 1);
+    mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&map64);
+    tma_prefetch_desc(&map16);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    if (lane == 0 && nt > 0) {
+      mbar_arrive_expect_tx(&bars->qfull, kLaQSmem * kLaQPanelBytes);
+      for (int p = 0; p < kLaQSmem; ++p)
+        tma_load_2d(smem + p * kLaQPanelBytes, &qmap, &bars->qfull, 64 * (kLaQTmem + p), static_cast<int>(grow0));
+      bool ok = true;
+      int issued = 0;
+      for (int i = 0; i < nt && ok; ++i) {
+        const int st = i & 1;
+        const uint32_t ph = (i >> 1) & 1;
+        int kind, a, cnt;
+        sp.tile(i0 + i, kind, a, cnt);
+        const int row = static_cast<int>(off + a + (kind ? kv : 0));
+        const int n16 = (cnt + 15) >> 4;
+        uint8_t* buf = smem + kLaOffBuf + st * kLaBuf;
+        for (int g = 0; g < 2; ++g) {                 // logit-only panels, then the value panels
+          uint64_t* full = g ? &bars->full_v[st] : &bars->full_t[st];
+          uint64_t* empty = g ? &bars->empty_v[st] : &bars->empty_t[st];
+          const int np = g ? kLaVPanels : kLaTPanels;
+          if (!mbar_wait(empty, ph ^ 1, abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(full, np * n16 * 2048);
+          issued = 2 * i + g + 1;
+          for (int p = 0; p < np; ++p) {
+            // value half 0 is panels 0-3, half 1 panels 4-7; panel 8 is rotary only
+            const int pnl = g ? 4 * vh + p : (vh == 0 ? 4 + p : (p < 4 ? p : 8));
+            uint8_t* dst = buf + (g ? p : kLaVPanels + p) * kLaPanelBytes;
+            if (n16 == 4) {
+              tma_load_2d(dst, &map64, full, 64 * pnl, row);
+            } else {
+              for (int c = 0; c < n16; ++c) tma_load_2d(dst + c * 2048, &map16, full, 64 * pnl, row + 16 * c);
+            }
+          }
+        }
+      }
+      // no copy is in flight when the CTA ends (matters after an abort only)
+      mbar_wait_drain(&bars->qfull, 0);
+      for (int k = issued > 4 ? issued - 4 : 0; k < issued; ++k) {
+        const int i = k >> 1;
+        mbar_wait_drain((k & 1) ? &bars->full_v[i & 1] : &bars->full_t[i & 1], (i >> 1) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, kLaVPanels * 64) | (1u << 16);   // B MN-major
+    bool ok = nt > 0;
+    if (ok) ok = warp_wait(&bars->qtmem, 0, abort_flag);
+    if (ok) ok = warp_wait(&bars->qfull, 0, abort_flag);
+    tc_fence_after();
+    int n16_prev = 0;
+    for (int i = 0; i <= nt && ok; ++i) {
+      int n16 = 0;
+      if (i < nt) {
+        const int st = i & 1;
+        const uint32_t ph = (i >> 1) & 1;
+        int kind, a, cnt;
+        sp.tile(i0 + i, kind, a, cnt);
+        n16 = (cnt + 15) >> 4;
+        const uint32_t idesc_s = idesc_bf16_f32(kLaRows, 16 * n16);
+        const uint32_t buf = base + static_cast<uint32_t>(kLaOffBuf) + st * kLaBuf;
+        const uint32_t d = tmem + kLaColS + 64 * st;
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (!warp_wait(g ? &bars->full_v[st] : &bars->full_t[st], ph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const int np = g ? kLaVPanels : kLaTPanels;
+          for (int p = 0; p < np; ++p) {
+            const int pnl = g ? 4 * vh + p : (vh == 0 ? 4 + p : (p < 4 ? p : 8));
+            const uint32_t kb = buf + (g ? p : kLaVPanels + p) * kLaPanelBytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t bdesc = sw128_kmajor_desc(kb + kk * 32);
+              const uint32_t acc = (g | p | kk) ? 1u : 0u;
+              if (pnl < kLaQTmem)
+                umma_f16_tmem_a_warp(d, tmem + kLaColQ + 32 * pnl + 8 * kk, bdesc, idesc_s, acc);
+              else
+                umma_f16_warp(d, sw128_kmajor_desc(base + (pnl - kLaQTmem) * kLaQPanelBytes + kk * 32), bdesc,
+                              idesc_s, acc);
+            }
+          }
+          if (g == 0) umma_commit_warp(&bars->empty_t[st]);
+        }
+        if (!ok) break;
+        umma_commit_warp(&bars->sfull[st]);
+      }
+      if (i > 0) {                                    // the output of the tile before
+        const int j = i - 1, st = j & 1;
+        if (!warp_wait(&bars->pfull[st], (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t vb = base + static_cast<uint32_t>(kLaOffBuf) + st * kLaBuf;
+        for (int s = 0; s < n16_prev; ++s)
+          umma_f16_tmem_a_warp(tmem + kLaColO, tmem + kLaColS + 64 * st + 8 * s,
+                               sw128_mnmajor_desc(vb + s * 2048, kLaPanelBytes), idesc_o, (j | s) ? 1u : 0u);
+        umma_commit_warp(&bars->empty_v[st]);
+        umma_commit_warp(&bars->odone);
+      }
+      n16_prev = n16;
+    }
+    // all MMAs this warp started are complete once `drain` flips
+    if (nt > 0) {
+      umma_commit_warp(&bars->drain);
+      if (lane == 0) mbar_wait_drain(&bars->drain, 0);
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int quad = warp & 3;                        // warps 2-5: tensor-memory lanes 32 * (warp & 3) ..
+    const int r = quad * 32 + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const bool live = r < nrows;
+    const int tok = static_cast<int>((r0 + (live ? r : nrows - 1)) / H);
+    bool ok = true;
+    if (nt > 0) {
+      // query panels 0-3 of this row into tensor memory
+      const uint4* src = reinterpret_cast<const uint4*>(P.q + (grow0 + r) * kAttnLatent);
+      for (int p = 0; p < kLaQTmem; ++p) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = live ? __ldg(src + 8 * p + c) : make_uint4(0u, 0u, 0u, 0u);
+          w[4 * c] = v.x;
+          w[4 * c + 1] = v.y;
+          w[4 * c + 2] = v.z;
+          w[4 * c + 3] = v.w;
+        }
+        tmem_st_32x32(trow + kLaColQ + 32 * p, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->qtmem);
+    }
+    // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
+    int hi, lo;
+    const uint64_t* branch = nullptr;
+    if (is_tree) {
+      branch = P.tree + static_cast<int64_t>(t0 + tok) * P.words;
+      int depth = 0;
+      if (P.window > 0) {
+        for (int w = 0; w < P.words; ++w) depth += __popcll(__ldg(branch + w) & la_low_mask(n - 64 * w));
+        depth = depth > 0 ? depth - 1 : 0;
+      }
+      hi = sp.hi;
+      lo = la_window_lo(kv + depth, P.window, P.align);
+    } else {
+      const int p = kv - n + tok;
+      hi = p + 1 < avail ? p + 1 : avail;
+      lo = la_window_lo(p, P.window, P.align);
+    }
+    const float sl2 = P.scale * 1.4426950408889634f;  // logits in log2 units
+    float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
+    for (int i = 0; i < nt; ++i) {
+      const int st = i & 1;
+      int kind, a, cnt;
+      sp.tile(i0 + i, kind, a, cnt);
+      const bool whole = kind == 0 && cnt == kLaTile && a + kLaTile <= sp.hi_min &&
+                         (a + kLaTile <= P.n_sink || a >= sp.lo_max);
+      uint64_t vis = ~0ull;
+      if (!whole) {
+        if (kind == 0)
+          vis = la_low_mask(hi - a < cnt ? hi - a : cnt) & (la_low_mask(P.n_sink - a) | ~la_low_mask(lo - a));
+        else
+          vis = __ldg(branch + (a >> 6)) & la_low_mask(cnt);
+      }
+      if (!warp_wait(&bars->sfull[st], (i >> 1) & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t va[32], vb[32];
+      const uint32_t scol = trow + kLaColS + 64 * st;
+      tmem_ld_32x32_nowait(scol, va);
+      tmem_ld_32x32_nowait(scol + 32, vb);
+      tmem_wait_ld(va);
+      tmem_wait_ld(vb);
+      if (!whole) {
+        const uint64_t hidden = ~vis & la_low_mask(16 * ((cnt + 15) >> 4));
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          bad |= ((hidden >> j) & 1ull) && (va[j] & 0x7f800000u) == 0x7f800000u;
+          bad |= ((hidden >> (j + 32)) & 1ull) && (vb[j] & 0x7f800000u) == 0x7f800000u;
+          if (!((vis >> j) & 1ull)) va[j] = 0xff800000u;
+          if (!((vis >> (j + 32)) & 1ull)) vb[j] = 0xff800000u;
+        }
+        // A row that holds something not finite gives every query row a logit that is not finite, so each
+        // warp finds out for its own query rows, and clears the staged values before its own arrival (two
+        // warps that clear the same piece store the same bytes).
+        if (__any_sync(0xffffffffu, bad)) {
+          uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffBuf + st * kLaBuf);
+          const int per_panel = ((cnt + 15) >> 4) * 128;   // 16-byte pieces of the staged rows of a panel
+          for (int e = lane; e < kLaVPanels * per_panel; e += 32) {
+            uint4* at = v4 + (e / per_panel) * (kLaPanelBytes / 16) + e % per_panel;
+            uint4 x = *at;
+            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((xw[k] & 0x7f80u) == 0x7f80u) xw[k] &= 0xffff0000u;
+              if ((xw[k] & 0x7f800000u) == 0x7f800000u) xw[k] &= 0x0000ffffu;
+            }
+            *at = x;
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      float mt = neg_inf();
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          mt = fmaxf(mt, fmaxf(sl2 * __uint_as_float(va[j]), sl2 * __uint_as_float(vb[j])));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if ((vis >> j) & 1ull) mt = fmaxf(mt, sl2 * __uint_as_float(va[j]));
+          if ((vis >> (j + 32)) & 1ull) mt = fmaxf(mt, sl2 * __uint_as_float(vb[j]));
+        }
+      }
+      const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? (m == neg_inf() ? 0.f : exp2f(m - mt)) : 1.f;
+        if (grow) m = mt;
+        l *= f;
+        lt *= f;
+        if (i > 0) {
+          if (!warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st_32x32(trow + kLaColO + 32 * c, o);
+          }
+        }
+      }
+      const float ref = m == neg_inf() ? 0.f : m;
+      float lp[4] = {0.f, 0.f, 0.f, 0.f}, ltp[4] = {0.f, 0.f, 0.f, 0.f};   // independent partial sums
+      uint32_t pw[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const uint32_t x0 = e < 16 ? va[2 * e] : vb[2 * e - 32];
+        const uint32_t x1 = e < 16 ? va[2 * e + 1] : vb[2 * e - 31];
+        float p0 = exp2f(fmaf(sl2, __uint_as_float(x0), -ref));
+        float p1 = exp2f(fmaf(sl2, __uint_as_float(x1), -ref));
+        if (!whole) {
+          if (!((vis >> (2 * e)) & 1ull)) p0 = 0.f;
+          if (!((vis >> (2 * e + 1)) & 1ull)) p1 = 0.f;
+        }
+        lp[e & 3] += p0 + p1;
+        const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+        ltp[e & 3] += __bfloat162float(pb.x) + __bfloat162float(pb.y);
+        pw[e] = *reinterpret_cast<const uint32_t*>(&pb);
+      }
+      l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      lt += (ltp[0] + ltp[1]) + (ltp[2] + ltp[3]);
+      tmem_st_32x32(scol, pw);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->pfull[st]);
+    }
+    // ------------------------------------------------------------ output
+    // The logits of the last tile say that the output of tile nt - 3 is complete, so its phase and the next
+    // one are waited for in turn (a wait for the last phase alone could meet the one two before it).
+    if (ok && nt > 1) ok = warp_wait(&bars->odone, (nt - 2) & 1, abort_flag);
+    if (ok && nt > 0) ok = warp_wait(&bars->odone, (nt - 1) & 1, abort_flag);
+    if (ok) {
+      tc_fence_after();
+      const bool empty = l == 0.f;                    // nothing visible (or only -inf logits)
+      const float inv = empty ? 0.f : 1.f / lt;
+      const int64_t row = grow0 + r;
+      const bool parts = P.n_split > 1;
+      if (vh == 0 && live) {
+        const float v = empty ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+        if (parts)
+          P.part_lse[static_cast<int64_t>(split) * P.T * H + row] = v;
+        else if (P.lse)
+          P.lse[row] = v;
+      }
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        if (nt > 0) {                                 // (uniform: the load is a warp's)
+          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
+          tmem_wait_ld(o);
+        }
+        if (!live || (parts && empty)) continue;      // an empty part is not read
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+        const int64_t at = row * kAttnValue + 256 * vh + 32 * c;
+        if (parts || !P.out_bf16) {
+          float* dst = parts ? P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue + at
+                             : static_cast<float*>(P.out) + at;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4*>(dst)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + at);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the split form: a block of 128 threads per row, four
+// value columns a thread; parts whose lse is -inf are not read.  Rows behind
+// the last sequence are left as they were.
+__global__ void __launch_bounds__(128)
+    latent_attn_combine_kernel(const __grid_constant__ LatentAttnParams P) {
+  const int64_t row = blockIdx.x;
+  const int64_t rows = static_cast<int64_t>(P.T) * P.H;
+  const int last = __ldg(P.q_start + P.B);
+  if (row < static_cast<int64_t>(__ldg(P.q_start)) * P.H || row >= static_cast<int64_t>(last) * P.H) return;
+  float m = neg_inf();
+  for (int s = 0; s < P.n_split; ++s) m = fmaxf(m, __ldg(P.part_lse + s * rows + row));
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < P.n_split; ++s) {
+    const float ls = __ldg(P.part_lse + s * rows + row);
+    if (ls == neg_inf()) continue;
+    const float w = expf(ls - m);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(P.part_o + (s * rows + row) * kAttnValue) + threadIdx.x);
+    den += w;
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  if (threadIdx.x == 0 && P.lse) P.lse[row] = den == 0.f ? neg_inf() : m + logf(den);
+  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (P.out_bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), c = __floats2bfloat162_rn(o.z, o.w);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * kAttnValue)[threadIdx.x] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+  } else {
+    reinterpret_cast<float4*>(static_cast<float*>(P.out) + row * kAttnValue)[threadIdx.x] = o;
+  }
+}
+
+cudaError_t launch_latent_attn(const CUtensorMap* qmap, const CUtensorMap* map64, const CUtensorMap* map16,
+                               const LatentAttnParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t e = smem_limit_once(attr_done, reinterpret_cast<const void*>(&latent_attn_kernel), kLaSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = static_cast<int64_t>(p.B) * p.max_tiles * p.n_split * 2;
+  latent_attn_kernel<<<static_cast<unsigned>(blocks), kLaThreads, kLaSmem, st>>>(*qmap, *map64, *map16, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_latent_attn_combine(const LatentAttnParams& p, cudaStream_t st) {
+  latent_attn_combine_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.T) * p.H), 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Number of CTA pairs that share one tile of query rows.  `pairs` pairs cover
+// the query rows, each over at most `tiles` tiles of the cache; the machine
+// runs 74 pairs at once.  A tile costs about 1 us, a pair about 6 tiles more
+// for its query, its first copies and its output, and the combine about 4
+// (with the launch): the split that makes the longest chain shortest.
+inline int la_splits(int64_t pairs, int64_t tiles) {
+  int best = 1;
+  int64_t best_cost = 0;
+  const int64_t most = tiles < kLaMaxSplit ? tiles : kLaMaxSplit;
+  for (int64_t s = 1; s <= (most > 1 ? most : 1); ++s) {
+    const int64_t waves = (pairs * s + 73) / 74;
+    const int64_t cost = waves * ((tiles + s - 1) / s + 6) + (s > 1 ? 4 : 0);
+    if (s == 1 || cost < best_cost) {
+      best = static_cast<int>(s);
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+}  // namespace lsi
