@@ -17,11 +17,13 @@
 //    would take all of them; a CTA therefore keeps half of the value columns
 //    (256) and two CTAs work on the same 128 query rows, each computing the
 //    logits;
-//  - of the query's nine 64-element panels four live in tensor memory as the
-//    MMAs' A operand and five in shared memory (80 KB); two tiles of the cache
-//    (2 x 72 KB) are in flight beside them.  A tile is staged once: its four
-//    value panels are read as K-major keys by the logits and as MN-major
-//    values by the output (the same bytes);
+//  - of the query's nine 64-element panels the four of this CTA's value half
+//    live in tensor memory as the MMAs' A operand and five in shared memory
+//    (80 KB); a tile's value panels stay until its output is accumulated
+//    (three tiles of them, 96 KB), the other five panels pass through a ring
+//    of six (48 KB), so copies run about a tile ahead.  A value panel is
+//    staged once: the logits read it as K-major keys and the output as
+//    MN-major values (the same bytes);
 //  - the logits of tile i + 1 are issued before the output of tile i, so the
 //    softmax of a tile runs beside the MMAs of the next;
 //  - the weights go back to tensor memory as bf16 (A operand of the output);
@@ -57,16 +59,18 @@ constexpr int kLaTPanels = 5;                         // panels only the logits 
 constexpr int kLaQTmem = 4;                           // query panels in tensor memory
 constexpr int kLaQSmem = 5;                           // query panels in shared memory
 constexpr int kLaQPanelBytes = kLaRows * 128;         // 16 KB
-constexpr int kLaBuf = (kLaVPanels + kLaTPanels) * kLaPanelBytes;   // 72 KB
+constexpr int kLaVBuf = kLaVPanels * kLaPanelBytes;  // 32 KB: the value panels of a tile
+constexpr int kLaVBufs = 3;
+constexpr int kLaTRing = 6;
 constexpr int kLaThreads = 6 * 32;                    // copies, MMA, 4 softmax / epilogue warps
 constexpr int kLaColO = 0, kLaColS = 256, kLaColQ = 384;            // tensor-memory columns
 constexpr float kLaLazy = 8.f;                        // log2 growth of a maximum that forces a rescale
 constexpr int kLaMaxSplit = 64;
 
 struct LaBars {
-  uint64_t qfull, qtmem;
-  uint64_t full_t[2], full_v[2];     // logit-only panels / value panels of a buffer have landed
-  uint64_t empty_t[2], empty_v[2];
+  uint64_t qfull, qstage, qtmem;     // query: shared-memory panels landed; staged ones landed; in tensor memory
+  uint64_t t_full[kLaTRing], t_empty[kLaTRing];
+  uint64_t v_full[kLaVBufs], v_empty[kLaVBufs];
   uint64_t sfull[2];                 // logits in tensor memory
   uint64_t pfull[2];                 // weights in tensor memory
   uint64_t odone;                    // output MMAs of a tile are complete
@@ -74,11 +78,16 @@ struct LaBars {
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kLaOffBuf = size_t(kLaQSmem) * kLaQPanelBytes;
-constexpr size_t kLaOffBars = kLaOffBuf + 2 * size_t(kLaBuf);
+constexpr size_t kLaOffV = size_t(kLaQSmem) * kLaQPanelBytes;
+constexpr size_t kLaOffT = kLaOffV + kLaVBufs * size_t(kLaVBuf);
+constexpr size_t kLaOffBars = kLaOffT + kLaTRing * size_t(kLaPanelBytes);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
+static_assert(kLaQTmem * kLaQPanelBytes <= 2 * kLaVBuf, "the staged query panels fit two value buffers");
+// the output's rows on their way out, a 16-byte pad apart (lanes on different banks)
+constexpr int kLaOutPitch16 = 256 * 2 + 16, kLaOutPitch32 = 256 * 4 + 16;
+static_assert(kLaRows * kLaOutPitch32 <= kLaVBufs * kLaVBuf + kLaTRing * kLaPanelBytes, "output rows fit the ring");
 
 struct LatentAttnParams {
   const uint16_t* q = nullptr;        // [T * H][576]
@@ -137,6 +146,122 @@ struct LaSpan {
     cnt = cnt < kLaTile ? cnt : kLaTile;
   }
 };
+
+// Panels of the latent row that a CTA of value half vh only reads as keys, and its value panels
+// (half 0: panels 0-3, half 1: panels 4-7; panel 8 is rotary only).
+__device__ __forceinline__ int la_v_panel(int vh, int p) { return 4 * vh + p; }
+__device__ __forceinline__ int la_t_panel(int vh, int p) { return p == 4 ? 8 : 4 * (1 - vh) + p; }
+
+// One panel of a tile: 64 rows in one copy, fewer in copies of 16.
+__device__ __forceinline__ void la_load_panel(uint8_t* dst, const CUtensorMap* map64, const CUtensorMap* map16,
+                                              uint64_t* bar, int x, int row, int n16) {
+  if (n16 == 4) {
+    tma_load_2d(dst, map64, bar, x, row);
+  } else {
+    for (int c = 0; c < n16; ++c) tma_load_2d(dst + c * 2048, map16, bar, x, row + 16 * c);
+  }
+}
+
+// 2^x: the hardware's approximation (relative error 2^-22; 0 below 2^-126).
+__device__ __forceinline__ float la_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void la_add2(uint64_t& acc, uint64_t v) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(v));
+}
+
+__device__ __forceinline__ float la_sum2(uint64_t v) {
+  float a, b;
+  unpack_f32x2(v, a, b);
+  return a + b;
+}
+
+// Four MMAs along one 64-element panel (K = 16 each): one election, the
+// descriptors stepped by 32 bytes.  A in shared memory (a_desc) ...
+__device__ __forceinline__ void la_mma_panel(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
+      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// ... and A in tensor memory (8 columns a step), B stepped by b_step.
+template <int B_STEP>
+__device__ __forceinline__ void la_mma_tmem_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(B_STEP / 16), "n"(2 * B_STEP / 16),
+      "n"(3 * B_STEP / 16)
+      : "memory");
+}
+
+// Shared-memory row to global memory, asynchronously (sizes and addresses multiples of 16).
+__device__ __forceinline__ void la_bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void la_bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// One row's largest logit of a tile in log2 units (masked places hold -inf).
+__device__ __forceinline__ float la_row_max(const uint32_t (&va)[32], const uint32_t (&vb)[32], float sl2) {
+  float x[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) x[j & 3] = fmaxf(x[j & 3], fmaxf(__uint_as_float(va[j]), __uint_as_float(vb[j])));
+  const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  return top == neg_inf() ? top : sl2 * top;
+}
+
+// One row's weights of a tile, packed to bf16 pairs, and their sums: of the weights and of the rounded weights.
+template <bool MASKED>
+__device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const uint32_t (&vb)[32], uint64_t vis,
+                                               float sl2, float ref, uint32_t (&pw)[32], float& l, float& lt) {
+  const uint64_t s2 = pack_f32x2(sl2, sl2), r2 = pack_f32x2(-ref, -ref);
+  uint64_t a[2] = {0ull, 0ull}, c[2] = {0ull, 0ull};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    uint64_t z = pack_f32x2(__uint_as_float(e < 16 ? va[2 * e] : vb[2 * e - 32]),
+                            __uint_as_float(e < 16 ? va[2 * e + 1] : vb[2 * e - 31]));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(z) : "l"(s2), "l"(r2));
+    float p0, p1;
+    unpack_f32x2(z, p0, p1);
+    p0 = la_exp2(p0);
+    p1 = la_exp2(p1);
+    if (MASKED) {
+      if (!((vis >> (2 * e)) & 1ull)) p0 = 0.f;
+      if (!((vis >> (2 * e + 1)) & 1ull)) p1 = 0.f;
+    }
+    la_add2(a[e & 1], pack_f32x2(p0, p1));
+    const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+    pw[e] = *reinterpret_cast<const uint32_t*>(&pb);
+    la_add2(c[e & 1], pack_f32x2(__uint_as_float(pw[e] << 16), __uint_as_float(pw[e] & 0xffff0000u)));
+  }
+  la_add2(a[0], a[1]);
+  la_add2(c[0], c[1]);
+  l += la_sum2(a[0]);
+  lt += la_sum2(c[0]);
+}
 
 // grid: B * max_tiles * n_split * 2 CTAs, the value half innermost.
 // qmap: q rows, box 64 x 128; map64 / map16: latent rows, boxes 64 x 64 and 64 x 16; 128-byte swizzle.
@@ -215,12 +340,17 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->qfull, 1);
+    mbar_init(&bars->qstage, 1);
     mbar_init(&bars->qtmem, 4);
+    for (int i = 0; i < kLaTRing; ++i) {
+      mbar_init(&bars->t_full[i], 1);
+      mbar_init(&bars->t_empty[i], 1);
+    }
+    for (int i = 0; i < kLaVBufs; ++i) {
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->full_t[i], 1);
-      mbar_init(&bars->full_v[i], 1);
-      mbar_init(&bars->empty_t[i], 1);
-      mbar_init(&bars->empty_v[i], 1);
       mbar_init(&bars->sfull[i], 1);
       mbar_init(&bars->pfull[i], 4);
     }
@@ -246,44 +376,47 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     if (lane == 0 && nt > 0) {
+      mbar_arrive_expect_tx(&bars->qstage, kLaQTmem * kLaQPanelBytes);
+      for (int p = 0; p < kLaQTmem; ++p)
+        tma_load_2d(smem + kLaOffV + p * kLaQPanelBytes, &qmap, &bars->qstage, 64 * la_v_panel(vh, p),
+                    static_cast<int>(grow0));
       mbar_arrive_expect_tx(&bars->qfull, kLaQSmem * kLaQPanelBytes);
       for (int p = 0; p < kLaQSmem; ++p)
-        tma_load_2d(smem + p * kLaQPanelBytes, &qmap, &bars->qfull, 64 * (kLaQTmem + p), static_cast<int>(grow0));
+        tma_load_2d(smem + p * kLaQPanelBytes, &qmap, &bars->qfull, 64 * la_t_panel(vh, p), static_cast<int>(grow0));
       bool ok = true;
-      int issued = 0;
+      int nT = 0, nV = 0;                             // panels and value buffers filled
+      int ts = 0, tph = 1, vs = 0, vph = 1;           // ring places and the parity that says they are free
       for (int i = 0; i < nt && ok; ++i) {
-        const int st = i & 1;
-        const uint32_t ph = (i >> 1) & 1;
         int kind, a, cnt;
         sp.tile(i0 + i, kind, a, cnt);
         const int row = static_cast<int>(off + a + (kind ? kv : 0));
         const int n16 = (cnt + 15) >> 4;
-        uint8_t* buf = smem + kLaOffBuf + st * kLaBuf;
-        for (int g = 0; g < 2; ++g) {                 // logit-only panels, then the value panels
-          uint64_t* full = g ? &bars->full_v[st] : &bars->full_t[st];
-          uint64_t* empty = g ? &bars->empty_v[st] : &bars->empty_t[st];
-          const int np = g ? kLaVPanels : kLaTPanels;
-          if (!mbar_wait(empty, ph ^ 1, abort_flag)) { ok = false; break; }
-          mbar_arrive_expect_tx(full, np * n16 * 2048);
-          issued = 2 * i + g + 1;
-          for (int p = 0; p < np; ++p) {
-            // value half 0 is panels 0-3, half 1 panels 4-7; panel 8 is rotary only
-            const int pnl = g ? 4 * vh + p : (vh == 0 ? 4 + p : (p < 4 ? p : 8));
-            uint8_t* dst = buf + (g ? p : kLaVPanels + p) * kLaPanelBytes;
-            if (n16 == 4) {
-              tma_load_2d(dst, &map64, full, 64 * pnl, row);
-            } else {
-              for (int c = 0; c < n16; ++c) tma_load_2d(dst + c * 2048, &map16, full, 64 * pnl, row + 16 * c);
-            }
-          }
+        for (int p = 0; p < kLaTPanels; ++p) {
+          if (!mbar_wait(&bars->t_empty[ts], tph, abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bars->t_full[ts], n16 * 2048);
+          la_load_panel(smem + kLaOffT + ts * kLaPanelBytes, &map64, &map16, &bars->t_full[ts],
+                        64 * la_t_panel(vh, p), row, n16);
+          ++nT;
+          if (++ts == kLaTRing) { ts = 0; tph ^= 1; }
         }
+        // the value buffers hold the query's staged panels first
+        if (ok && i == 0) ok = mbar_wait(&bars->qtmem, 0, abort_flag);
+        if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bars->v_full[vs], kLaVPanels * n16 * 2048);
+        for (int p = 0; p < kLaVPanels; ++p)
+          la_load_panel(smem + kLaOffV + vs * kLaVBuf + p * kLaPanelBytes, &map64, &map16, &bars->v_full[vs],
+                        64 * la_v_panel(vh, p), row, n16);
+        ++nV;
+        if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
       }
       // no copy is in flight when the CTA ends (matters after an abort only)
+      mbar_wait_drain(&bars->qstage, 0);
       mbar_wait_drain(&bars->qfull, 0);
-      for (int k = issued > 4 ? issued - 4 : 0; k < issued; ++k) {
-        const int i = k >> 1;
-        mbar_wait_drain((k & 1) ? &bars->full_v[i & 1] : &bars->full_t[i & 1], (i >> 1) & 1);
-      }
+      for (int k = nT > kLaTRing ? nT - kLaTRing : 0; k < nT; ++k)
+        mbar_wait_drain(&bars->t_full[k % kLaTRing], (k / kLaTRing) & 1);
+      for (int k = nV > kLaVBufs ? nV - kLaVBufs : 0; k < nV; ++k)
+        mbar_wait_drain(&bars->v_full[k % kLaVBufs], (k / kLaVBufs) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -294,52 +427,54 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (ok) ok = warp_wait(&bars->qfull, 0, abort_flag);
     tc_fence_after();
     int n16_prev = 0;
+    int ts = 0, tph = 0, vs = 0, vph = 0, vprev = 0;
     for (int i = 0; i <= nt && ok; ++i) {
       int n16 = 0;
+      const int vcur = vs;
       if (i < nt) {
         const int st = i & 1;
-        const uint32_t ph = (i >> 1) & 1;
         int kind, a, cnt;
         sp.tile(i0 + i, kind, a, cnt);
         n16 = (cnt + 15) >> 4;
         const uint32_t idesc_s = idesc_bf16_f32(kLaRows, 16 * n16);
-        const uint32_t buf = base + static_cast<uint32_t>(kLaOffBuf) + st * kLaBuf;
         const uint32_t d = tmem + kLaColS + 64 * st;
-        for (int g = 0; g < 2 && ok; ++g) {
-          if (!warp_wait(g ? &bars->full_v[st] : &bars->full_t[st], ph, abort_flag)) { ok = false; break; }
+        for (int p = 0; p < kLaTPanels; ++p) {
+          if (!warp_wait(&bars->t_full[ts], tph, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const int np = g ? kLaVPanels : kLaTPanels;
-          for (int p = 0; p < np; ++p) {
-            const int pnl = g ? 4 * vh + p : (vh == 0 ? 4 + p : (p < 4 ? p : 8));
-            const uint32_t kb = buf + (g ? p : kLaVPanels + p) * kLaPanelBytes;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t bdesc = sw128_kmajor_desc(kb + kk * 32);
-              const uint32_t acc = (g | p | kk) ? 1u : 0u;
-              if (pnl < kLaQTmem)
-                umma_f16_tmem_a_warp(d, tmem + kLaColQ + 32 * pnl + 8 * kk, bdesc, idesc_s, acc);
-              else
-                umma_f16_warp(d, sw128_kmajor_desc(base + (pnl - kLaQTmem) * kLaQPanelBytes + kk * 32), bdesc,
-                              idesc_s, acc);
-            }
-          }
-          if (g == 0) umma_commit_warp(&bars->empty_t[st]);
+          la_mma_panel(d, sw128_kmajor_desc(base + p * kLaQPanelBytes),
+                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + ts * kLaPanelBytes), idesc_s,
+                       p ? 1u : 0u);
+          umma_commit_warp(&bars->t_empty[ts]);
+          if (++ts == kLaTRing) { ts = 0; tph ^= 1; }
         }
+        if (ok) ok = warp_wait(&bars->v_full[vs], vph, abort_flag);
         if (!ok) break;
+        tc_fence_after();
+        const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vs * kLaVBuf;
+#pragma unroll
+        for (int p = 0; p < kLaVPanels; ++p)
+          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * kLaPanelBytes), idesc_s, 1u);
         umma_commit_warp(&bars->sfull[st]);
+        if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
       }
       if (i > 0) {                                    // the output of the tile before
         const int j = i - 1, st = j & 1;
         if (!warp_wait(&bars->pfull[st], (j >> 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t vb = base + static_cast<uint32_t>(kLaOffBuf) + st * kLaBuf;
-        for (int s = 0; s < n16_prev; ++s)
-          umma_f16_tmem_a_warp(tmem + kLaColO, tmem + kLaColS + 64 * st + 8 * s,
-                               sw128_mnmajor_desc(vb + s * 2048, kLaPanelBytes), idesc_o, (j | s) ? 1u : 0u);
-        umma_commit_warp(&bars->empty_v[st]);
+        const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vprev * kLaVBuf;
+        const uint32_t a_tmem = tmem + kLaColS + 64 * st;
+        const uint64_t bdesc = sw128_mnmajor_desc(vb, kLaPanelBytes);
+        if (n16_prev == 4) {
+          la_mma_tmem_x4<2048>(tmem + kLaColO, a_tmem, bdesc, idesc_o, j ? 1u : 0u);
+        } else {
+          for (int s = 0; s < n16_prev; ++s)
+            umma_f16_tmem_a_warp(tmem + kLaColO, a_tmem + 8 * s, bdesc + s * (2048 / 16), idesc_o, (j | s) ? 1u : 0u);
+        }
+        umma_commit_warp(&bars->v_empty[vprev]);
         umma_commit_warp(&bars->odone);
       }
       n16_prev = n16;
+      vprev = vcur;
     }
     // all MMAs this warp started are complete once `drain` flips
     if (nt > 0) {
@@ -356,13 +491,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int tok = static_cast<int>((r0 + (live ? r : nrows - 1)) / H);
     bool ok = true;
     if (nt > 0) {
-      // query panels 0-3 of this row into tensor memory
-      const uint4* src = reinterpret_cast<const uint4*>(P.q + (grow0 + r) * kAttnLatent);
-      for (int p = 0; p < kLaQTmem; ++p) {
+      // the staged query panels of this row into tensor memory
+      ok = warp_wait(&bars->qstage, 0, abort_flag);
+      for (int p = 0; p < kLaQTmem && ok; ++p) {
         uint32_t w[32];
+        const uint8_t* src = smem + kLaOffV + p * kLaQPanelBytes + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-          const uint4 v = live ? __ldg(src + 8 * p + c) : make_uint4(0u, 0u, 0u, 0u);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4));
           w[4 * c] = v.x;
           w[4 * c + 1] = v.y;
           w[4 * c + 2] = v.z;
@@ -392,9 +528,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       hi = p + 1 < avail ? p + 1 : avail;
       lo = la_window_lo(p, P.window, P.align);
     }
-    const float sl2 = P.scale * 1.4426950408889634f;  // logits in log2 units
+    // logits in log2 units; below 0 the logits' signs are turned instead
+    const bool turn = P.scale < 0.f;
+    const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
     float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
-    for (int i = 0; i < nt; ++i) {
+    int vs = 0;
+    for (int i = 0; i < nt && ok; ++i) {
       const int st = i & 1;
       int kind, a, cnt;
       sp.tile(i0 + i, kind, a, cnt);
@@ -415,6 +554,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       tmem_ld_32x32_nowait(scol + 32, vb);
       tmem_wait_ld(va);
       tmem_wait_ld(vb);
+      if (turn) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          va[j] ^= 0x80000000u;
+          vb[j] ^= 0x80000000u;
+        }
+      }
       if (!whole) {
         const uint64_t hidden = ~vis & la_low_mask(16 * ((cnt + 15) >> 4));
         bool bad = false;
@@ -429,7 +575,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // warp finds out for its own query rows, and clears the staged values before its own arrival (two
         // warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
-          uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffBuf + st * kLaBuf);
+          uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + vs * kLaVBuf);
           const int per_panel = ((cnt + 15) >> 4) * 128;   // 16-byte pieces of the staged rows of a panel
           for (int e = lane; e < kLaVPanels * per_panel; e += 32) {
             uint4* at = v4 + (e / per_panel) * (kLaPanelBytes / 16) + e % per_panel;
@@ -445,21 +591,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           fence_proxy_async_smem();
         }
       }
-      float mt = neg_inf();
-      if (whole) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          mt = fmaxf(mt, fmaxf(sl2 * __uint_as_float(va[j]), sl2 * __uint_as_float(vb[j])));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if ((vis >> j) & 1ull) mt = fmaxf(mt, sl2 * __uint_as_float(va[j]));
-          if ((vis >> (j + 32)) & 1ull) mt = fmaxf(mt, sl2 * __uint_as_float(vb[j]));
-        }
-      }
+      const float mt = la_row_max(va, vb, sl2);
       const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? (m == neg_inf() ? 0.f : exp2f(m - mt)) : 1.f;
+        const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
         if (grow) m = mt;
         l *= f;
         lt *= f;
@@ -477,30 +612,17 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       const float ref = m == neg_inf() ? 0.f : m;
-      float lp[4] = {0.f, 0.f, 0.f, 0.f}, ltp[4] = {0.f, 0.f, 0.f, 0.f};   // independent partial sums
       uint32_t pw[32];
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const uint32_t x0 = e < 16 ? va[2 * e] : vb[2 * e - 32];
-        const uint32_t x1 = e < 16 ? va[2 * e + 1] : vb[2 * e - 31];
-        float p0 = exp2f(fmaf(sl2, __uint_as_float(x0), -ref));
-        float p1 = exp2f(fmaf(sl2, __uint_as_float(x1), -ref));
-        if (!whole) {
-          if (!((vis >> (2 * e)) & 1ull)) p0 = 0.f;
-          if (!((vis >> (2 * e + 1)) & 1ull)) p1 = 0.f;
-        }
-        lp[e & 3] += p0 + p1;
-        const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-        ltp[e & 3] += __bfloat162float(pb.x) + __bfloat162float(pb.y);
-        pw[e] = *reinterpret_cast<const uint32_t*>(&pb);
-      }
-      l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
-      lt += (ltp[0] + ltp[1]) + (ltp[2] + ltp[3]);
+      if (whole)
+        la_row_weights<false>(va, vb, vis, sl2, ref, pw, l, lt);
+      else
+        la_row_weights<true>(va, vb, vis, sl2, ref, pw, l, lt);
       tmem_st_32x32(scol, pw);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->pfull[st]);
+      if (++vs == kLaVBufs) vs = 0;
     }
     // ------------------------------------------------------------ output
     // The logits of the last tile say that the output of tile nt - 3 is complete, so its phase and the next
@@ -520,35 +642,49 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         else if (P.lse)
           P.lse[row] = v;
       }
+      // rows through shared memory (free now: every copy and MMA of the CTA is done), so that each leaves as
+      // one copy of its 512 or 1024 bytes
+      const bool wide = parts || !P.out_bf16;
+      uint8_t* stage = smem + kLaOffV + r * (wide ? kLaOutPitch32 : kLaOutPitch16);
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
-        __syncwarp();
-        if (nt > 0) {                                 // (uniform: the load is a warp's)
+        if (nt > 0) {
           tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
           tmem_wait_ld(o);
         }
-        if (!live || (parts && empty)) continue;      // an empty part is not read
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
-        const int64_t at = row * kAttnValue + 256 * vh + 32 * c;
-        if (parts || !P.out_bf16) {
-          float* dst = parts ? P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue + at
-                             : static_cast<float*>(P.out) + at;
+        if (wide) {
+          uint4* dst = reinterpret_cast<uint4*>(stage + 128 * c);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            reinterpret_cast<uint4*>(dst)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else {
-          uint32_t w[16];
+          uint4* dst = reinterpret_cast<uint4*>(stage + 64 * c);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __nv_bfloat162 h =
+                  __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * x]), __uint_as_float(o[8 * k + 2 * x + 1]));
+              w[x] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + at);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
       }
+      fence_proxy_async_smem();
+      if (live && !(parts && empty)) {                // an empty part is not read
+        const int64_t at = row * kAttnValue + 256 * vh;
+        if (parts)
+          la_bulk_store(P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue + at, stage, 1024);
+        else if (wide)
+          la_bulk_store(static_cast<float*>(P.out) + at, stage, 1024);
+        else
+          la_bulk_store(static_cast<uint16_t*>(P.out) + at, stage, 512);
+        la_bulk_store_wait();
+      }
+      __syncwarp();
     }
   }
 
