@@ -20,15 +20,18 @@
 //  - of the query's nine 64-element panels the four of this CTA's value half
 //    live in tensor memory as the MMAs' A operand and five in shared memory
 //    (80 KB); a tile's value panels stay until its output is accumulated
-//    (three tiles of them, 96 KB), the other five panels pass through a ring
-//    of six (48 KB), so copies run about a tile ahead.  A value panel is
-//    staged once: the logits read it as K-major keys and the output as
-//    MN-major values (the same bytes);
+//    (three tiles of them, 96 KB); the other five have one place each (40 KB),
+//    free for the next tile as soon as the logits passed them.  The logits
+//    take the value panels first, so both kinds of copies run about 1500
+//    cycles ahead.  A value panel is staged once: the logits read it as
+//    K-major keys and the output as MN-major values (the same bytes);
 //  - the logits of tile i + 1 are issued before the output of tile i, so the
 //    softmax of a tile runs beside the MMAs of the next;
 //  - the weights go back to tensor memory as bf16 (A operand of the output);
-//    the output is rescaled only when a row's maximum grew by more than 8
-//    (in log2 units: weights stay below 2^8, so nothing overflows).
+//    the output is rescaled only when a row's maximum grew by more than 16
+//    (in log2 units: weights stay below 2^16, which neither bf16 nor fp32
+//    holds less exactly than weights below 1); the sinks, a few rows, come
+//    after the window, so that the first reference is the maximum of many.
 //
 // Rounding to fewer bits: the weights (bf16, half a step is 2^-8 of a weight; the sum that
 // divides the output is that of the rounded weights, so they still sum to 1)
@@ -61,15 +64,16 @@ constexpr int kLaQSmem = 5;                           // query panels in shared 
 constexpr int kLaQPanelBytes = kLaRows * 128;         // 16 KB
 constexpr int kLaVBuf = kLaVPanels * kLaPanelBytes;  // 32 KB: the value panels of a tile
 constexpr int kLaVBufs = 3;
-constexpr int kLaTRing = 6;
+constexpr int kLaTFirst = 3;                          // key-only panels freed by a commit of their own
 constexpr int kLaThreads = 6 * 32;                    // copies, MMA, 4 softmax / epilogue warps
 constexpr int kLaColO = 0, kLaColS = 256, kLaColQ = 384;            // tensor-memory columns
-constexpr float kLaLazy = 8.f;                        // log2 growth of a maximum that forces a rescale
+constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
 constexpr int kLaMaxSplit = 64;
 
 struct LaBars {
   uint64_t qfull, qstage, qtmem;     // query: shared-memory panels landed; staged ones landed; in tensor memory
-  uint64_t t_full[kLaTRing], t_empty[kLaTRing];
+  uint64_t t_full;                   // a tile's key-only panels have landed (two arrivals)
+  uint64_t t_empty[2];               // the first three, the last two are read
   uint64_t v_full[kLaVBufs], v_empty[kLaVBufs];
   uint64_t sfull[2];                 // logits in tensor memory
   uint64_t pfull[2];                 // weights in tensor memory
@@ -80,14 +84,14 @@ struct LaBars {
 };
 constexpr size_t kLaOffV = size_t(kLaQSmem) * kLaQPanelBytes;
 constexpr size_t kLaOffT = kLaOffV + kLaVBufs * size_t(kLaVBuf);
-constexpr size_t kLaOffBars = kLaOffT + kLaTRing * size_t(kLaPanelBytes);
+constexpr size_t kLaOffBars = kLaOffT + kLaTPanels * size_t(kLaPanelBytes);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
 static_assert(kLaQTmem * kLaQPanelBytes <= 2 * kLaVBuf, "the staged query panels fit two value buffers");
 // the output's rows on their way out, a 16-byte pad apart (lanes on different banks)
 constexpr int kLaOutPitch16 = 256 * 2 + 16, kLaOutPitch32 = 256 * 4 + 16;
-static_assert(kLaRows * kLaOutPitch32 <= kLaVBufs * kLaVBuf + kLaTRing * kLaPanelBytes, "output rows fit the ring");
+static_assert(kLaRows * kLaOutPitch32 <= kLaVBufs * kLaVBuf + kLaTPanels * kLaPanelBytes, "output rows fit the ring");
 
 struct LatentAttnParams {
   const uint16_t* q = nullptr;        // [T * H][576]
@@ -130,14 +134,13 @@ struct LaSpan {
   __device__ __forceinline__ int tiles() const { return n0 + n1 + n2; }
   // kind 0: rows a .. a + cnt of the sequence; 1: drafted rows a .. a + cnt
   __device__ __forceinline__ void tile(int i, int& kind, int& a, int& cnt) const {
-    if (i < n0) {
-      kind = 0;
-      a = kLaTile * i;
-      cnt = sink_len - a;
-    } else if (i < n0 + n1) {
-      kind = 0;
-      a = lo + kLaTile * (i - n0);
+    kind = 0;
+    if (i < n1) {
+      a = lo + kLaTile * i;
       cnt = hi - a;
+    } else if (i < n0 + n1) {
+      a = kLaTile * (i - n1);
+      cnt = sink_len - a;
     } else {
       kind = 1;
       a = kLaTile * (i - n0 - n1);
@@ -160,6 +163,14 @@ __device__ __forceinline__ void la_load_panel(uint8_t* dst, const CUtensorMap* m
   } else {
     for (int c = 0; c < n16; ++c) tma_load_2d(dst + c * 2048, map16, bar, x, row + 16 * c);
   }
+}
+
+// Warp-uniform bounded wait in which every lane tests the barrier: when the
+// phase is complete already, the common case of the MMA warp, it costs one
+// test and a vote.
+__device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort_flag);
 }
 
 // 2^x: the hardware's approximation (relative error 2^-22; 0 below 2^-126).
@@ -224,6 +235,19 @@ __device__ __forceinline__ void la_bulk_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
+// Sets the masked places of 32 logits to -inf; whether one of them (among the
+// places `there` that the MMAs wrote) was not finite.
+__device__ __forceinline__ bool la_mask_row(uint32_t (&v)[32], uint32_t vis, uint32_t there) {
+  const uint32_t hidden = there & ~vis;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (hidden & (1u << j)) bad |= (v[j] & 0x7f800000u) == 0x7f800000u;
+    if (!(vis & (1u << j))) v[j] = 0xff800000u;
+  }
+  return bad;
+}
+
 // One row's largest logit of a tile in log2 units (masked places hold -inf).
 __device__ __forceinline__ float la_row_max(const uint32_t (&va)[32], const uint32_t (&vb)[32], float sl2) {
   float x[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
@@ -234,9 +258,11 @@ __device__ __forceinline__ float la_row_max(const uint32_t (&va)[32], const uint
 }
 
 // One row's weights of a tile, packed to bf16 pairs, and their sums: of the weights and of the rounded weights.
+// Masked places hold -inf and weigh 0 (a scale of 0 takes them out by the mask: 0 * -inf is NaN).
 template <bool MASKED>
 __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const uint32_t (&vb)[32], uint64_t vis,
                                                float sl2, float ref, uint32_t (&pw)[32], float& l, float& lt) {
+  const uint32_t vlo = static_cast<uint32_t>(vis), vhi = static_cast<uint32_t>(vis >> 32);
   const uint64_t s2 = pack_f32x2(sl2, sl2), r2 = pack_f32x2(-ref, -ref);
   uint64_t a[2] = {0ull, 0ull}, c[2] = {0ull, 0ull};
 #pragma unroll
@@ -249,8 +275,9 @@ __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const u
     p0 = la_exp2(p0);
     p1 = la_exp2(p1);
     if (MASKED) {
-      if (!((vis >> (2 * e)) & 1ull)) p0 = 0.f;
-      if (!((vis >> (2 * e + 1)) & 1ull)) p1 = 0.f;
+      const uint32_t w = e < 16 ? vlo : vhi;
+      if (!(w & (1u << ((2 * e) & 31)))) p0 = 0.f;
+      if (!(w & (1u << ((2 * e + 1) & 31)))) p1 = 0.f;
     }
     la_add2(a[e & 1], pack_f32x2(p0, p1));
     const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
@@ -342,10 +369,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     mbar_init(&bars->qfull, 1);
     mbar_init(&bars->qstage, 1);
     mbar_init(&bars->qtmem, 4);
-    for (int i = 0; i < kLaTRing; ++i) {
-      mbar_init(&bars->t_full[i], 1);
-      mbar_init(&bars->t_empty[i], 1);
-    }
+    mbar_init(&bars->t_full, 2);
+    mbar_init(&bars->t_empty[0], 1);
+    mbar_init(&bars->t_empty[1], 1);
     for (int i = 0; i < kLaVBufs; ++i) {
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 1);
@@ -384,37 +410,44 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       for (int p = 0; p < kLaQSmem; ++p)
         tma_load_2d(smem + p * kLaQPanelBytes, &qmap, &bars->qfull, 64 * la_t_panel(vh, p), static_cast<int>(grow0));
       bool ok = true;
-      int nT = 0, nV = 0;                             // panels and value buffers filled
-      int ts = 0, tph = 1, vs = 0, vph = 1;           // ring places and the parity that says they are free
+      int nT = 0, nV = 0;                             // arrivals on t_full, value buffers filled
+      int vs = 0, vph = 1;                            // value buffer and the parity that says it is free
       for (int i = 0; i < nt && ok; ++i) {
         int kind, a, cnt;
         sp.tile(i0 + i, kind, a, cnt);
         const int row = static_cast<int>(off + a + (kind ? kv : 0));
         const int n16 = (cnt + 15) >> 4;
-        for (int p = 0; p < kLaTPanels; ++p) {
-          if (!mbar_wait(&bars->t_empty[ts], tph, abort_flag)) { ok = false; break; }
-          mbar_arrive_expect_tx(&bars->t_full[ts], n16 * 2048);
-          la_load_panel(smem + kLaOffT + ts * kLaPanelBytes, &map64, &map16, &bars->t_full[ts],
-                        64 * la_t_panel(vh, p), row, n16);
-          ++nT;
-          if (++ts == kLaTRing) { ts = 0; tph ^= 1; }
+        // the value buffers hold the query's staged panels first; the first tile's other panels need not wait
+        for (int g = 0; g < 3 && ok; ++g) {
+          const int what = i == 0 ? (g < 2 ? g : 2) : (g == 0 ? 2 : g - 1);   // 0, 1: key-only panels; 2: values
+          if (what == 2) {
+            if (i == 0) ok = mbar_wait(&bars->qtmem, 0, abort_flag);
+            if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars->v_full[vs], kLaVPanels * n16 * 2048);
+            for (int p = 0; p < kLaVPanels; ++p)
+              la_load_panel(smem + kLaOffV + vs * kLaVBuf + p * kLaPanelBytes, &map64, &map16, &bars->v_full[vs],
+                            64 * la_v_panel(vh, p), row, n16);
+            ++nV;
+            if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
+          } else {
+            const int p0 = what ? kLaTFirst : 0, p1 = what ? kLaTPanels : kLaTFirst;
+            ok = mbar_wait(&bars->t_empty[what], (i & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bars->t_full, (p1 - p0) * n16 * 2048);
+            for (int p = p0; p < p1; ++p)
+              la_load_panel(smem + kLaOffT + p * kLaPanelBytes, &map64, &map16, &bars->t_full,
+                            64 * la_t_panel(vh, p), row, n16);
+            ++nT;
+          }
         }
-        // the value buffers hold the query's staged panels first
-        if (ok && i == 0) ok = mbar_wait(&bars->qtmem, 0, abort_flag);
-        if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&bars->v_full[vs], kLaVPanels * n16 * 2048);
-        for (int p = 0; p < kLaVPanels; ++p)
-          la_load_panel(smem + kLaOffV + vs * kLaVBuf + p * kLaPanelBytes, &map64, &map16, &bars->v_full[vs],
-                        64 * la_v_panel(vh, p), row, n16);
-        ++nV;
-        if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
       }
-      // no copy is in flight when the CTA ends (matters after an abort only)
+      // no copy is in flight when the CTA ends (matters after an abort only; a tile whose second half was never
+      // asked for cannot complete its phase, so its first half is given the second's arrival)
       mbar_wait_drain(&bars->qstage, 0);
       mbar_wait_drain(&bars->qfull, 0);
-      for (int k = nT > kLaTRing ? nT - kLaTRing : 0; k < nT; ++k)
-        mbar_wait_drain(&bars->t_full[k % kLaTRing], (k / kLaTRing) & 1);
+      if (nT & 1) mbar_arrive(&bars->t_full);
+      if (nT > 0) mbar_wait_drain(&bars->t_full, ((nT - 1) >> 1) & 1);
       for (int k = nV > kLaVBufs ? nV - kLaVBufs : 0; k < nV; ++k)
         mbar_wait_drain(&bars->v_full[k % kLaVBufs], (k / kLaVBufs) & 1);
     }
@@ -427,7 +460,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (ok) ok = warp_wait(&bars->qfull, 0, abort_flag);
     tc_fence_after();
     int n16_prev = 0;
-    int ts = 0, tph = 0, vs = 0, vph = 0, vprev = 0;
+    int vs = 0, vph = 0, vprev = 0;
     for (int i = 0; i <= nt && ok; ++i) {
       int n16 = 0;
       const int vcur = vs;
@@ -438,28 +471,28 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         n16 = (cnt + 15) >> 4;
         const uint32_t idesc_s = idesc_bf16_f32(kLaRows, 16 * n16);
         const uint32_t d = tmem + kLaColS + 64 * st;
-        for (int p = 0; p < kLaTPanels; ++p) {
-          if (!warp_wait(&bars->t_full[ts], tph, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          la_mma_panel(d, sw128_kmajor_desc(base + p * kLaQPanelBytes),
-                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + ts * kLaPanelBytes), idesc_s,
-                       p ? 1u : 0u);
-          umma_commit_warp(&bars->t_empty[ts]);
-          if (++ts == kLaTRing) { ts = 0; tph ^= 1; }
-        }
-        if (ok) ok = warp_wait(&bars->v_full[vs], vph, abort_flag);
-        if (!ok) break;
+        if (!la_wait_all(&bars->v_full[vs], vph, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vs * kLaVBuf;
 #pragma unroll
         for (int p = 0; p < kLaVPanels; ++p)
-          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * kLaPanelBytes), idesc_s, 1u);
+          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * kLaPanelBytes), idesc_s,
+                             p ? 1u : 0u);
+        if (!la_wait_all(&bars->t_full, i & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < kLaTPanels; ++p) {
+          la_mma_panel(d, sw128_kmajor_desc(base + p * kLaQPanelBytes),
+                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + p * kLaPanelBytes), idesc_s, 1u);
+          if (p == kLaTFirst - 1) umma_commit_warp(&bars->t_empty[0]);
+        }
         umma_commit_warp(&bars->sfull[st]);
+        umma_commit_warp(&bars->t_empty[1]);
         if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
       }
       if (i > 0) {                                    // the output of the tile before
         const int j = i - 1, st = j & 1;
-        if (!warp_wait(&bars->pfull[st], (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        if (!la_wait_all(&bars->pfull[st], (j >> 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vprev * kLaVBuf;
         const uint32_t a_tmem = tmem + kLaColS + 64 * st;
@@ -562,15 +595,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       if (!whole) {
-        const uint64_t hidden = ~vis & la_low_mask(16 * ((cnt + 15) >> 4));
-        bool bad = false;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          bad |= ((hidden >> j) & 1ull) && (va[j] & 0x7f800000u) == 0x7f800000u;
-          bad |= ((hidden >> (j + 32)) & 1ull) && (vb[j] & 0x7f800000u) == 0x7f800000u;
-          if (!((vis >> j) & 1ull)) va[j] = 0xff800000u;
-          if (!((vis >> (j + 32)) & 1ull)) vb[j] = 0xff800000u;
-        }
+        const uint64_t there = la_low_mask(16 * ((cnt + 15) >> 4));
+        const bool bad = la_mask_row(va, static_cast<uint32_t>(vis), static_cast<uint32_t>(there)) |
+                         la_mask_row(vb, static_cast<uint32_t>(vis >> 32), static_cast<uint32_t>(there >> 32));
         // A row that holds something not finite gives every query row a logit that is not finite, so each
         // warp finds out for its own query rows, and clears the staged values before its own arrival (two
         // warps that clear the same piece store the same bytes).
