@@ -1666,6 +1666,22 @@ int tree_splits(int B, int H, int max_q, int64_t n_rows, int max_ctx, int window
                    span_tiles(H, max_q, ctx, window, align, n_sink, max_q));
 }
 
+// 3-D bf16 map over rows of 576 elements as [panel of 64][row][64 elements], box = 64 x box_rows x box_panels,
+// 128-byte swizzle: one copy stages whole panels one after another.
+ls_status make_panel_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_panels) {
+  auto fn = encode_fn();
+  if (!fn) return fail(LS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(kAttnLatent / 64)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(kAttnLatent * 2), 128};
+  cuuint32_t box[3] = {64u, box_rows, box_panels};
+  cuuint32_t es[3] = {1u, 1u, 1u};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(LS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return LS_OK;
+}
+
 // Shared checks, tensor maps and launches of the two span attentions.
 ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* latent, int max_q, int out_dtype,
                          void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -1690,14 +1706,18 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
     p.part_o = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H * kAttnValue);
     p.part_lse = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H);
   }
-  CUtensorMap qmap, map64, map16;
-  ls_status s = make_latent_map(&qmap, p.q, static_cast<uint64_t>(p.T) * p.H, kLaRows);
-  if (s == LS_OK) s = make_latent_map(&map64, latent, static_cast<uint64_t>(p.n_rows), kLaTile);
-  if (s == LS_OK) s = make_latent_map(&map16, latent, static_cast<uint64_t>(p.n_rows), 16);
+  LaMaps maps;
+  const uint64_t q_rows = static_cast<uint64_t>(p.T) * p.H, kv_rows = static_cast<uint64_t>(p.n_rows);
+  ls_status s = make_panel_map(&maps.q4, p.q, q_rows, kLaRows, 4);
+  if (s == LS_OK) s = make_panel_map(&maps.q1, p.q, q_rows, kLaRows, 1);
+  if (s == LS_OK) s = make_panel_map(&maps.kv4, latent, kv_rows, kLaTile, 4);
+  if (s == LS_OK) s = make_panel_map(&maps.kv1, latent, kv_rows, kLaTile, 1);
+  if (s == LS_OK) s = make_panel_map(&maps.few4, latent, kv_rows, 16, 4);
+  if (s == LS_OK) s = make_panel_map(&maps.few1, latent, kv_rows, 16, 1);
   if (s != LS_OK) return s;
   {
     ProfScope prof("latent_attn_kernel", st);
-    LS_CUDA(launch_latent_attn(&qmap, &map64, &map16, p, st));
+    LS_CUDA(launch_latent_attn(maps, p, st));
   }
   if (p.n_split > 1) {
     ProfScope prof("latent_attn_combine_kernel", st);

@@ -21,7 +21,9 @@
 //    live in tensor memory as the MMAs' A operand and five in shared memory
 //    (80 KB); a tile's value panels stay until its output is accumulated
 //    (three tiles of them, 96 KB); the other five have one place each (40 KB),
-//    free for the next tile as soon as the logits passed them.  The logits
+//    free for the next tile as soon as the logits passed them.  A copy takes
+//    four panels at once (a 3-D box of 64 elements x rows x panels): with one
+//    panel a copy the issue alone took 2000 of a tile's 3200 cycles.  The logits
 //    take the value panels first, so both kinds of copies run about 1500
 //    cycles ahead.  A value panel is staged once: the logits read it as
 //    K-major keys and the output as MN-major values (the same bytes);
@@ -64,7 +66,7 @@ constexpr int kLaQSmem = 5;                           // query panels in shared 
 constexpr int kLaQPanelBytes = kLaRows * 128;         // 16 KB
 constexpr int kLaVBuf = kLaVPanels * kLaPanelBytes;  // 32 KB: the value panels of a tile
 constexpr int kLaVBufs = 3;
-constexpr int kLaTFirst = 3;                          // key-only panels freed by a commit of their own
+constexpr int kLaTFirst = 4;                          // key-only panels freed by a commit of their own
 constexpr int kLaThreads = 6 * 32;                    // copies, MMA, 4 softmax / epilogue warps
 constexpr int kLaColO = 0, kLaColS = 256, kLaColQ = 384;            // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
@@ -73,7 +75,7 @@ constexpr int kLaMaxSplit = 64;
 struct LaBars {
   uint64_t qfull, qstage, qtmem;     // query: shared-memory panels landed; staged ones landed; in tensor memory
   uint64_t t_full;                   // a tile's key-only panels have landed (two arrivals)
-  uint64_t t_empty[2];               // the first three, the last two are read
+  uint64_t t_empty[2];               // the first four, the last one are read
   uint64_t v_full[kLaVBufs], v_empty[kLaVBufs];
   uint64_t sfull[2];                 // logits in tensor memory
   uint64_t pfull[2];                 // weights in tensor memory
@@ -150,20 +152,22 @@ struct LaSpan {
   }
 };
 
-// Panels of the latent row that a CTA of value half vh only reads as keys, and its value panels
-// (half 0: panels 0-3, half 1: panels 4-7; panel 8 is rotary only).
-__device__ __forceinline__ int la_v_panel(int vh, int p) { return 4 * vh + p; }
-__device__ __forceinline__ int la_t_panel(int vh, int p) { return p == 4 ? 8 : 4 * (1 - vh) + p; }
+// First of the four value panels of a CTA of value half vh, first of the four that it only reads as keys besides
+// panel 8 (rotary): half 0 has the values of panels 0-3, half 1 those of panels 4-7.
+__device__ __forceinline__ int la_v_panel(int vh) { return 4 * vh; }
+__device__ __forceinline__ int la_t_panel(int vh) { return 4 - 4 * vh; }
 
-// One panel of a tile: 64 rows in one copy, fewer in copies of 16.
-__device__ __forceinline__ void la_load_panel(uint8_t* dst, const CUtensorMap* map64, const CUtensorMap* map16,
-                                              uint64_t* bar, int x, int row, int n16) {
-  if (n16 == 4) {
-    tma_load_2d(dst, map64, bar, x, row);
-  } else {
-    for (int c = 0; c < n16; ++c) tma_load_2d(dst + c * 2048, map16, bar, x, row + 16 * c);
-  }
+// Box of 64 elements x rows x panels: x in elements of a panel, y the row, z the panel.
+__device__ __forceinline__ void la_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(z)
+      : "memory");
 }
+
+// Rows of a tile as they are staged: 64, or 16 for a tile of at most 16 (panels lie that many rows apart).
+__device__ __forceinline__ int la_box_rows(int cnt) { return cnt <= 16 ? 16 : kLaTile; }
 
 // Warp-uniform bounded wait in which every lane tests the barrier: when the
 // phase is complete already, the common case of the MMA warp, it costs one
@@ -290,11 +294,16 @@ __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const u
   lt += la_sum2(c[0]);
 }
 
+// Tensor maps over rows of 9 panels of 64 elements, boxes of 64 elements x rows x panels, 128-byte swizzle.
+struct LaMaps {
+  CUtensorMap q4, q1;       // q rows: 128 x 4 panels, 128 x 1
+  CUtensorMap kv4, kv1;     // latent rows: 64 x 4, 64 x 1
+  CUtensorMap few4, few1;   // latent rows: 16 x 4, 16 x 1
+};
+
 // grid: B * max_tiles * n_split * 2 CTAs, the value half innermost.
-// qmap: q rows, box 64 x 128; map64 / map16: latent rows, boxes 64 x 64 and 64 x 16; 128-byte swizzle.
 __global__ void __launch_bounds__(kLaThreads, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap map64,
-                       const __grid_constant__ CUtensorMap map16, const __grid_constant__ LatentAttnParams P) {
+    latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
   extern __shared__ uint8_t la_raw[];
   uint8_t* smem = smem_align1024(la_raw);
   LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
@@ -390,9 +399,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&map64);
-    tma_prefetch_desc(&map16);
+    tma_prefetch_desc(&M.q4);
+    tma_prefetch_desc(&M.q1);
+    tma_prefetch_desc(&M.kv4);
+    tma_prefetch_desc(&M.kv1);
   }
   tc_fence_before();
   __syncthreads();
@@ -403,12 +413,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // ------------------------------------------------------------ copies
     if (lane == 0 && nt > 0) {
       mbar_arrive_expect_tx(&bars->qstage, kLaQTmem * kLaQPanelBytes);
-      for (int p = 0; p < kLaQTmem; ++p)
-        tma_load_2d(smem + kLaOffV + p * kLaQPanelBytes, &qmap, &bars->qstage, 64 * la_v_panel(vh, p),
-                    static_cast<int>(grow0));
+      la_load_3d(smem + kLaOffV, &M.q4, &bars->qstage, static_cast<int>(grow0), la_v_panel(vh));
       mbar_arrive_expect_tx(&bars->qfull, kLaQSmem * kLaQPanelBytes);
-      for (int p = 0; p < kLaQSmem; ++p)
-        tma_load_2d(smem + p * kLaQPanelBytes, &qmap, &bars->qfull, 64 * la_t_panel(vh, p), static_cast<int>(grow0));
+      la_load_3d(smem, &M.q4, &bars->qfull, static_cast<int>(grow0), la_t_panel(vh));
+      la_load_3d(smem + 4 * kLaQPanelBytes, &M.q1, &bars->qfull, static_cast<int>(grow0), 8);
       bool ok = true;
       int nT = 0, nV = 0;                             // arrivals on t_full, value buffers filled
       int vs = 0, vph = 1;                            // value buffer and the parity that says it is free
@@ -416,28 +424,29 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         int kind, a, cnt;
         sp.tile(i0 + i, kind, a, cnt);
         const int row = static_cast<int>(off + a + (kind ? kv : 0));
-        const int n16 = (cnt + 15) >> 4;
+        const int box = la_box_rows(cnt);
+        const CUtensorMap* four = box == kLaTile ? &M.kv4 : &M.few4;
+        const CUtensorMap* one = box == kLaTile ? &M.kv1 : &M.few1;
         // the value buffers hold the query's staged panels first; the first tile's other panels need not wait
         for (int g = 0; g < 3 && ok; ++g) {
-          const int what = i == 0 ? (g < 2 ? g : 2) : (g == 0 ? 2 : g - 1);   // 0, 1: key-only panels; 2: values
+          const int what = i == 0 ? g : g == 0 ? 2 : g - 1;   // 0, 1: key-only panels; 2: values
           if (what == 2) {
             if (i == 0) ok = mbar_wait(&bars->qtmem, 0, abort_flag);
             if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
             if (!ok) break;
-            mbar_arrive_expect_tx(&bars->v_full[vs], kLaVPanels * n16 * 2048);
-            for (int p = 0; p < kLaVPanels; ++p)
-              la_load_panel(smem + kLaOffV + vs * kLaVBuf + p * kLaPanelBytes, &map64, &map16, &bars->v_full[vs],
-                            64 * la_v_panel(vh, p), row, n16);
+            mbar_arrive_expect_tx(&bars->v_full[vs], 4 * box * 128);
+            la_load_3d(smem + kLaOffV + vs * kLaVBuf, four, &bars->v_full[vs], row, la_v_panel(vh));
             ++nV;
             if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
           } else {
-            const int p0 = what ? kLaTFirst : 0, p1 = what ? kLaTPanels : kLaTFirst;
             ok = mbar_wait(&bars->t_empty[what], (i & 1) ^ 1, abort_flag);
             if (!ok) break;
-            mbar_arrive_expect_tx(&bars->t_full, (p1 - p0) * n16 * 2048);
-            for (int p = p0; p < p1; ++p)
-              la_load_panel(smem + kLaOffT + p * kLaPanelBytes, &map64, &map16, &bars->t_full,
-                            64 * la_t_panel(vh, p), row, n16);
+            uint8_t* dst = smem + kLaOffT;
+            mbar_arrive_expect_tx(&bars->t_full, (what ? 1 : 4) * box * 128);
+            if (what == 0)
+              la_load_3d(dst, four, &bars->t_full, row, la_t_panel(vh));
+            else
+              la_load_3d(dst + kLaTFirst * box * 128, one, &bars->t_full, row, 8);
             ++nT;
           }
         }
@@ -471,19 +480,20 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         n16 = (cnt + 15) >> 4;
         const uint32_t idesc_s = idesc_bf16_f32(kLaRows, 16 * n16);
         const uint32_t d = tmem + kLaColS + 64 * st;
+        const uint32_t pitch = la_box_rows(cnt) * 128;   // bytes between panels
         if (!la_wait_all(&bars->v_full[vs], vph, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vs * kLaVBuf;
 #pragma unroll
         for (int p = 0; p < kLaVPanels; ++p)
-          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * kLaPanelBytes), idesc_s,
+          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * pitch), idesc_s,
                              p ? 1u : 0u);
         if (!la_wait_all(&bars->t_full, i & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
         for (int p = 0; p < kLaTPanels; ++p) {
           la_mma_panel(d, sw128_kmajor_desc(base + p * kLaQPanelBytes),
-                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + p * kLaPanelBytes), idesc_s, 1u);
+                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + p * pitch), idesc_s, 1u);
           if (p == kLaTFirst - 1) umma_commit_warp(&bars->t_empty[0]);
         }
         umma_commit_warp(&bars->sfull[st]);
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         tc_fence_after();
         const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vprev * kLaVBuf;
         const uint32_t a_tmem = tmem + kLaColS + 64 * st;
-        const uint64_t bdesc = sw128_mnmajor_desc(vb, kLaPanelBytes);
+        const uint64_t bdesc = sw128_mnmajor_desc(vb, n16_prev == 1 ? 16 * 128 : kLaPanelBytes);
         if (n16_prev == 4) {
           la_mma_tmem_x4<2048>(tmem + kLaColO, a_tmem, bdesc, idesc_o, j ? 1u : 0u);
         } else {
@@ -603,9 +613,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
           uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + vs * kLaVBuf);
-          const int per_panel = ((cnt + 15) >> 4) * 128;   // 16-byte pieces of the staged rows of a panel
-          for (int e = lane; e < kLaVPanels * per_panel; e += 32) {
-            uint4* at = v4 + (e / per_panel) * (kLaPanelBytes / 16) + e % per_panel;
+          for (int e = lane; e < kLaVPanels * 8 * la_box_rows(cnt); e += 32) {
+            uint4* at = v4 + e;
             uint4 x = *at;
             uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -760,13 +769,12 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-cudaError_t launch_latent_attn(const CUtensorMap* qmap, const CUtensorMap* map64, const CUtensorMap* map16,
-                               const LatentAttnParams& p, cudaStream_t st) {
+cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = smem_limit_once(attr_done, reinterpret_cast<const void*>(&latent_attn_kernel), kLaSmem);
   if (e != cudaSuccess) return e;
   const int64_t blocks = static_cast<int64_t>(p.B) * p.max_tiles * p.n_split * 2;
-  latent_attn_kernel<<<static_cast<unsigned>(blocks), kLaThreads, kLaSmem, st>>>(*qmap, *map64, *map16, p);
+  latent_attn_kernel<<<static_cast<unsigned>(blocks), kLaThreads, kLaSmem, st>>>(maps, p);
   return cudaGetLastError();
 }
 
