@@ -12,14 +12,17 @@
 //          for the pairs (2i, 2i + 1), interleaved, or (i, i + rope / 2)
 //   fp8: scale = max |y| / 448 (1 for a row of zeros), code = e4m3(y / scale)
 //
-// Bound by bytes: every element is read and written once.  A warp takes one
-// row at a time, 8 elements (16 bytes) of it per lane and step, held in
-// registers as fp32 between the two passes that a norm needs; only the
-// rotation's partners cross lanes, through the warp's own strip of shared
-// memory.  The angle is formed in 64 bits (at a position of ten million an
-// fp32 product is off by a radian) and reduced to half turns before the fp32
-// sine and cosine; a block works on the heads of one token, so that an angle
-// is computed once per block and not per head.
+// Bound by bytes: every element is read and written once; what has to stay
+// small beside them is the number of instructions per row.  LPR lanes (8, 16
+// or 32, whichever leaves the fewest idle) share a row, each holding STEPS
+// pieces of 8 elements in fp32 between the passes that a norm needs.  A block
+// works on heads of one token: its angles are formed once (in 64 bits: at a
+// position of ten million an fp32 product is off by a radian; reduced to half
+// turns before the fp32 sine and cosine), and a lane keeps those of its pieces
+// in registers for all its rows.  Where the rotated part is whole pieces of
+// one step (kAligned), a rotation's partners are in the same piece
+// (interleaved) or in the same registers of another lane, one shuffle away;
+// any other offset goes through a strip of shared memory.
 
 #pragma once
 
@@ -28,7 +31,7 @@
 namespace lsi {
 
 constexpr int kNrMaxDim = 1024;
-constexpr int kNrWarps = 8;
+constexpr int kNrWarps = 4;
 constexpr int kNrMaxRope = 256;
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
@@ -55,173 +58,289 @@ struct NormRopeParams {
   int blocks_per_token = 1;
 };
 
-__device__ __forceinline__ float nr_warp_sum(float v) {
+template <int LPR>
+__device__ __forceinline__ float nr_row_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float nr_warp_max(float v) {
+template <int LPR>
+__device__ __forceinline__ float nr_row_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-// STEPS = ceil(d / 256): 16-byte pieces per lane.
-template <int STEPS>
+__device__ __forceinline__ void nr_load8(float (&w)[8], const float* __restrict__ p) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = __ldg(p + k);
+}
+
+// One row (LPR lanes of the warp; the others work on other rows): norm, rotation, store.
+// `on`: the row exists and is written; every lane takes part in the shuffles.
+template <int LPR, int STEPS, bool ALIGNED>
+__device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS][8], int lane_in, int part, int h,
+                                       int64_t orow, bool on, const float (&rc)[8], const float (&rsn)[8],
+                                       int rope_step, float* strip, const float* s_cos, const float* s_sin) {
+  const NormRows& R = P.part[part];
+  const int pieces = P.d >> 3;
+  const int np = P.norm_dim >> 3;                     // norm_dim is a multiple of 8: whole pieces
+  const int half = P.rope >> 1;
+  if (P.part[0].norm | P.part[1].norm) {
+    const bool norm = R.norm != NORM_NONE;
+    const float inv_n = 1.f / static_cast<float>(P.norm_dim > 0 ? P.norm_dim : 1);
+    float mu = 0.f;
+    if (P.part[0].norm == NORM_LAYER || P.part[1].norm == NORM_LAYER) {
+      float a = 0.f;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+        if (LPR * s + lane_in < np) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a += x[s][k];
+        }
+      a = nr_row_sum<LPR>(a) * inv_n;
+      if (R.norm == NORM_LAYER) mu = a;
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+      if (LPR * s + lane_in < np) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[s][k] -= mu;
+          q = fmaf(x[s][k], x[s][k], q);
+        }
+      }
+    q = nr_row_sum<LPR>(q);
+    if (norm) {
+      const float rs = 1.f / sqrtf(q * inv_n + P.eps);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int c = LPR * s + lane_in;
+        if (c < np) {
+          float w[8];
+          if (R.weight) {
+            nr_load8(w, R.weight + 8 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[s][k] *= rs * w[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[s][k] *= rs;
+          }
+          if (R.bias) {
+            nr_load8(w, R.bias + 8 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[s][k] += w[k];
+          }
+        }
+      }
+    }
+  }
+  if (ALIGNED) {
+    // the step that holds the rotated part; the pieces outside it stay as they are (an infinity too)
+    if (half > 0) {
+      const int j = LPR * rope_step + lane_in - (P.rope_off >> 3);   // piece of the rotated part
+      const bool rotated = j >= 0 && 8 * j < P.rope;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        if (s != rope_step) continue;
+        if (P.interleaved) {
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            const float a = x[s][k], b = x[s][k + 1];
+            if (rotated) {
+              x[s][k] = fmaf(a, rc[k], -(b * rsn[k]));
+              x[s][k + 1] = fmaf(b, rc[k], a * rsn[k]);
+            }
+          }
+        } else {
+          const int hp = half >> 3;
+          const bool second = j >= hp;
+          const int partner = !rotated ? lane_in : second ? lane_in - hp : lane_in + hp;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float other = __shfl_sync(0xffffffffu, x[s][k], partner, LPR);
+            if (rotated)
+              x[s][k] = second ? fmaf(x[s][k], rc[k], other * rsn[k]) : fmaf(x[s][k], rc[k], -(other * rsn[k]));
+          }
+        }
+      }
+    }
+  } else {
+    // through the row's strip, so that any pairing and any offset is a plain read
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = LPR * s + lane_in;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = 8 * c + k - P.rope_off;
+        if (c < pieces && i >= 0 && i < P.rope) strip[i] = x[s][k];
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = LPR * s + lane_in;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = 8 * c + k - P.rope_off;
+        if (c < pieces && i >= 0 && i < P.rope) {
+          const bool second = P.interleaved ? (i & 1) : (i >= half);
+          const int pair = P.interleaved ? (i >> 1) : (second ? i - half : i);
+          const float other = strip[P.interleaved ? (i ^ 1) : (second ? i - half : i + half)];
+          const float co = s_cos[pair], si = s_sin[pair];
+          x[s][k] = second ? fmaf(x[s][k], co, other * si) : fmaf(x[s][k], co, -(other * si));
+        }
+      }
+    }
+    __syncwarp();
+  }
+  const int64_t at = orow * R.heads + h;
+  if (P.fp8) {
+    float top = 0.f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[s][k]));
+    top = nr_row_max<LPR>(top);
+    const float sc = top > 0.f ? top / 448.f : 1.f;
+    const float inv = 1.f / sc;                       // the quotient to fp32 rounding, far below an e4m3 step
+    if (on && lane_in == 0) R.scale[at] = sc;
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(R.out) + at * P.d);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = LPR * s + lane_in;
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint16_t two;                                 // high byte: the first operand
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+            : "=h"(two)
+            : "f"(x[s][2 * k + 1] * inv), "f"(x[s][2 * k] * inv));
+        w[k >> 1] |= static_cast<uint32_t>(two) << (16 * (k & 1));
+      }
+      if (on && c < pieces) dst[c] = make_uint2(w[0], w[1]);
+    }
+  } else {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(R.out) + at * P.d);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = LPR * s + lane_in;
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[s][2 * k], x[s][2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if (on && c < pieces) dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+template <int LPR, int STEPS, bool ALIGNED>
 __global__ void __launch_bounds__(kNrWarps * 32)
     norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
+  constexpr int kRows = 32 / LPR;                     // rows a warp works on at once
+  constexpr int kDeep = STEPS == 1 ? 2 : 1;           // and one after another, their loads issued together
   __shared__ float s_cos[kNrMaxRope / 2], s_sin[kNrMaxRope / 2];
-  __shared__ float s_mid[kNrWarps][kNrMaxRope];
+  __shared__ float s_strip[ALIGNED ? 1 : kNrWarps * kRows][ALIGNED ? 1 : kNrMaxRope];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane_in = lane % LPR, sub = lane / LPR;
   const int t = blockIdx.x / P.blocks_per_token;
   const int h0 = (blockIdx.x - t * P.blocks_per_token) * P.chunk;
-  const int half = P.rope / 2;
-  {
-    const int64_t pos = half > 0 ? __ldg(P.pos + t) : 0;
+  const int pieces = P.d >> 3;
+  const int heads = P.part[0].heads + P.part[1].heads;
+  const int h_end = h0 + P.chunk < heads ? h0 + P.chunk : heads;
+  const int half = P.rope >> 1;
+
+  const int stride = kNrWarps * kRows;
+  uint4 raw[kDeep][STEPS];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int hh = base + u * stride;
+      const bool in = hh < h_end;
+      const int part = in && hh >= P.part[0].heads ? 1 : 0;
+      const NormRows& R = P.part[part];
+      const int h = part ? hh - P.part[0].heads : hh;
+      const uint4* src = reinterpret_cast<const uint4*>(R.x + t * R.x_stride + static_cast<int64_t>(h) * P.d);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int c = LPR * s + lane_in;
+        raw[u][s] = in && c < pieces ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  const int first = h0 + warp * kRows + sub;
+  fetch(first);                                       // in flight while the angles are formed
+  if (half > 0) {
+    const int64_t pos = __ldg(P.pos + t);
     for (int i = threadIdx.x; i < half; i += kNrWarps * 32) {
       // the angle in half turns, reduced to [-1, 1]
-      const double half_turns = static_cast<double>(pos) * static_cast<double>(__ldg(P.inv_freq + i)) * 0.31830988618379067;
+      const double half_turns =
+          static_cast<double>(pos) * static_cast<double>(__ldg(P.inv_freq + i)) * 0.31830988618379067;
       const double r = half_turns - 2.0 * rint(0.5 * half_turns);
       sincospif(static_cast<float>(r), &s_sin[i], &s_cos[i]);
     }
   }
   __syncthreads();
-  const int pieces = P.d >> 3;
-  const int heads = P.part[0].heads + P.part[1].heads;
-  const int h_end = h0 + P.chunk < heads ? h0 + P.chunk : heads;
-  for (int hh = h0 + warp; hh < h_end; hh += kNrWarps) {
-    const bool second = hh >= P.part[0].heads;
-    const NormRows& R = P.part[second ? 1 : 0];
-    const int h = second ? hh - P.part[0].heads : hh;
-    int64_t orow = t;
-    if (R.slots) {
-      orow = __ldg(R.slots + t);
-      if (orow < 0 || orow >= R.out_rows) {           // -1: the token has no row
-        if (orow != -1 && lane == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
-        continue;
-      }
-    }
-    const uint4* src = reinterpret_cast<const uint4*>(R.x + t * R.x_stride + static_cast<int64_t>(h) * P.d);
-    float x[STEPS][8];
+  // the cosines and sines of this lane's piece of the rotated step (ALIGNED)
+  float rc[8], rsn[8];
+  const int rope_step = ALIGNED ? (P.rope_off >> 3) / LPR : 0;
+  if (ALIGNED) {
+    const int j = LPR * rope_step + lane_in - (P.rope_off >> 3);
+    const bool in = j >= 0 && 8 * j < P.rope;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int c = 32 * s + lane;
-      const uint4 v = c < pieces ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[s][2 * k] = __uint_as_float(w[k] << 16);
-        x[s][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-      }
-    }
-    if (R.norm != NORM_NONE) {                        // norm_dim is a multiple of 8: whole pieces
-      const int np = P.norm_dim >> 3;
-      const float inv_n = 1.f / static_cast<float>(P.norm_dim);
-      float mu = 0.f;
-      if (R.norm == NORM_LAYER) {
-        float a = 0.f;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-          if (32 * s + lane < np) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a += x[s][k];
-          }
-        mu = nr_warp_sum(a) * inv_n;
-      }
-      float q = 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-        if (32 * s + lane < np) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[s][k] -= mu;
-            q = fmaf(x[s][k], x[s][k], q);
-          }
-        }
-      const float rs = 1.f / sqrtf(nr_warp_sum(q) * inv_n + P.eps);
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = 32 * s + lane;
-        if (c < np) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float y = x[s][k] * rs;
-            if (R.weight) y *= __ldg(R.weight + 8 * c + k);
-            if (R.bias) y += __ldg(R.bias + 8 * c + k);
-            x[s][k] = y;
-          }
-        }
-      }
-    }
-    if (half > 0) {
-      // the rotated part through the warp's strip, so that any pairing and any offset is a plain read
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = 32 * s + lane;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = 8 * c + k - P.rope_off;
-          if (c < pieces && i >= 0 && i < P.rope) s_mid[warp][i] = x[s][k];
-        }
-      }
-      __syncwarp();
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = 32 * s + lane;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = 8 * c + k - P.rope_off;
-          if (c < pieces && i >= 0 && i < P.rope) {
-            const bool hi = P.interleaved ? (i & 1) : (i >= half);
-            const int pair = P.interleaved ? (i >> 1) : (hi ? i - half : i);
-            const float other = s_mid[warp][P.interleaved ? (i ^ 1) : (hi ? i - half : i + half)];
-            const float co = s_cos[pair], si = s_sin[pair];
-            x[s][k] = hi ? fmaf(x[s][k], co, other * si) : fmaf(x[s][k], co, -(other * si));
-          }
-        }
-      }
-      __syncwarp();
-    }
-    const int64_t at = orow * R.heads + h;
-    if (P.fp8) {
-      float top = 0.f;
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[s][k]));
-      top = nr_warp_max(top);
-      const float sc = top > 0.f ? top / 448.f : 1.f;
-      if (lane == 0) R.scale[at] = sc;
-      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(R.out) + at * P.d);
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = 32 * s + lane;
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint16_t two;                               // d.hi = e4m3(a), d.lo = e4m3(b)
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-              : "=h"(two)
-              : "f"(x[s][2 * k + 1] / sc), "f"(x[s][2 * k] / sc));
-          w[k >> 1] |= static_cast<uint32_t>(two) << (16 * (k & 1));
-        }
-        if (c < pieces) dst[c] = make_uint2(w[0], w[1]);
-      }
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(R.out) + at * P.d);
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = 32 * s + lane;
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x[s][2 * k], x[s][2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        if (c < pieces) dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const int pair = P.interleaved ? 4 * j + (k >> 1) : (8 * j + k) % (half > 0 ? half : 1);
+      rc[k] = in ? s_cos[in ? pair : 0] : 1.f;
+      rsn[k] = in ? s_sin[in ? pair : 0] : 0.f;
     }
   }
+  for (int base = first - sub; base < h_end; base += kDeep * stride) {
+    if (base != first - sub) fetch(base + sub);
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int hh = base + sub + u * stride;
+      if (base + u * stride >= h_end) break;          // (uniform over the warp)
+      const bool in = hh < h_end;
+      const int part = in && hh >= P.part[0].heads ? 1 : 0;
+      const int h = part ? hh - P.part[0].heads : hh;
+      int64_t orow = t;
+      bool on = in;
+      if (part && P.part[1].slots) orow = __ldg(P.part[1].slots + t);
+      if (!part && P.part[0].slots) orow = __ldg(P.part[0].slots + t);
+      if (in && P.part[part].slots && (orow < 0 || orow >= P.part[part].out_rows)) {   // -1: the token has no row
+        if (orow != -1 && lane_in == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
+        on = false;
+      }
+      if (!on) orow = 0;
+      float x[STEPS][8];
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const uint32_t w[4] = {raw[u][s].x, raw[u][s].y, raw[u][s].z, raw[u][s].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[s][2 * k] = __uint_as_float(w[k] << 16);
+          x[s][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+      }
+      nr_row<LPR, STEPS, ALIGNED>(P, x, lane_in, part, h, orow, on, rc, rsn, rope_step,
+                                  s_strip[ALIGNED ? 0 : warp * kRows + sub], s_cos, s_sin);
+    }
+  }
+}
+
+template <int LPR, int STEPS>
+inline void nr_launch(const NormRopeParams& p, unsigned blocks, cudaStream_t st) {
+  // the rotated part is whole pieces of one step (interleaved pairs lie inside a piece anyway)
+  const int piece = p.rope_off >> 3, last = (p.rope_off + p.rope - 1) >> 3;
+  const bool aligned = p.rope == 0 || (p.rope_off % 8 == 0 && p.rope % (p.interleaved ? 8 : 16) == 0 &&
+                                       piece / LPR == last / LPR);
+  if (aligned)
+    norm_rope_kernel<LPR, STEPS, true><<<blocks, kNrWarps * 32, 0, st>>>(p);
+  else
+    norm_rope_kernel<LPR, STEPS, false><<<blocks, kNrWarps * 32, 0, st>>>(p);
 }
 
 cudaError_t launch_norm_rope(const NormRopeParams& p0, int num_sms, cudaStream_t st) {
@@ -230,17 +349,19 @@ cudaError_t launch_norm_rope(const NormRopeParams& p0, int num_sms, cudaStream_t
   if (p.T == 0 || heads == 0) return cudaSuccess;
   // a block takes all heads of a token unless the tokens alone would leave SMs without a block
   int split = 1;
-  while (static_cast<int64_t>(p.T) * split < num_sms && split * kNrWarps < heads) split *= 2;
+  while (static_cast<int64_t>(p.T) * split < 2 * num_sms && split * kNrWarps < heads) split *= 2;
   p.chunk = (heads + split - 1) / split;
   p.blocks_per_token = (heads + p.chunk - 1) / p.chunk;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.T) * p.blocks_per_token);
-  const int threads = kNrWarps * 32;
-  switch ((p.d + 255) / 256) {
-    case 1: norm_rope_kernel<1><<<blocks, threads, 0, st>>>(p); break;
-    case 2: norm_rope_kernel<2><<<blocks, threads, 0, st>>>(p); break;
-    case 3: norm_rope_kernel<3><<<blocks, threads, 0, st>>>(p); break;
-    default: norm_rope_kernel<4><<<blocks, threads, 0, st>>>(p); break;
-  }
+  // lanes per row and pieces per lane: the fewest idle lanes for d / 8 pieces
+  const int pieces = p.d / 8;
+  if (pieces <= 8) nr_launch<8, 1>(p, blocks, st);
+  else if (pieces <= 16) nr_launch<16, 1>(p, blocks, st);
+  else if (pieces <= 24) nr_launch<8, 3>(p, blocks, st);
+  else if (pieces <= 32) nr_launch<32, 1>(p, blocks, st);
+  else if (pieces <= 64) nr_launch<32, 2>(p, blocks, st);
+  else if (pieces <= 72) nr_launch<8, 9>(p, blocks, st);
+  else nr_launch<32, 4>(p, blocks, st);
   return cudaGetLastError();
 }
 

@@ -149,6 +149,21 @@ def test_rows_of_zeros_and_nan(L):
         assert torch.isnan(y[2, 0, 3 if norm == "none" else 100].float()) and torch.isfinite(y[:2].float()).all()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("off", [0, 8, 32, 5])
+def test_elements_outside_the_rotation(L, off, interleaved):
+    """Elements outside the rotated part keep their values, infinities and NaN among them (a NaN comes back as the
+    conversion's own, 0x7fff: PTX cvt to bf16x2 keeps no payload)."""
+    g = torch.Generator().manual_seed(off)
+    x = torch.randn(3, 5, 128, generator=g).to(torch.bfloat16).cuda()
+    x[:, :, 100], x[:, :, 110], x[:, 2, 90] = float("inf"), float("nan"), -float("inf")
+    f = torch.ones(16, device="cuda")
+    y = L.ls_norm_rope(x, None, torch.arange(3, device="cuda") + 1, f, rope_off=off, interleaved=interleaved)[0]
+    same = ((y.view(torch.int16) == x.view(torch.int16)) | (torch.isnan(x) & torch.isnan(y))).cpu()
+    assert same[:, :, :off].all() and same[:, :, off + 32:].all() and not same[:, :, off:off + 32].all()
+    assert torch.isfinite(y[:, :, off:off + 32].float()).all()
+
+
 def test_graph_and_stream(L):
     s = make(9, 32, 1, 128, 64, 128, seed=6)
     want = L.ls_norm_rope(s["q"], s["k"], s["pos"], s["inv_freq"], q_norm="rms", k_norm="rms", fp8=True)
