@@ -9,6 +9,7 @@ shared library and raises ImportError when it is missing or stale.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -663,62 +664,97 @@ def ls_attention_merge(o_parts, lse_parts, out=None, stream=None):
     return o, lse
 
 
+# The span attentions and the norm are called once per layer and token, so their binding is kept short: one test per
+# tensor for what it has to be (`_fits`), and the words of a refusal only when it fails.
+_HERE = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _on(t: torch.Tensor, stream):
     """Context in which a call's outputs and workspace are allocated and its kernels launched: t's device, and
     `stream` (default: the device's current one), so that scratch memory belongs to the stream that uses it."""
-    if t.device.type != "cuda":
-        raise ValueError("q must be a CUDA tensor")
-    if stream is None:
-        return torch.cuda.device(t.device)
-    if stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    return torch.cuda.stream(stream)
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
-def _together(ref: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {ref.device}")
+def _fits(t, dtype, ndim: int, index: int, name: str) -> int:
+    """Address of t, a contiguous `ndim`-d tensor of `dtype` on CUDA device `index`."""
+    if not (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index):
+        _dev(t, dtype, name, ndim)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    return t.data_ptr()
 
 
-def _span_args(q, latent, q_start, lens, row_off, max_q, scale, out_dtype, out, want_lse, lens_name):
-    """Checks and outputs that the two span attentions share -> (max_q, scale, out dtype code, out, lse)."""
-    _dev(q, torch.bfloat16, "q", 3)
-    _dev(latent, torch.bfloat16, "latent", 2)
-    _dev(q_start, torch.int32, "q_start", 1)
-    _dev(lens, torch.int32, lens_name, 1)
-    _opt(row_off, torch.int64, "row_off")
-    T, H, d = q.shape
-    B = lens.shape[0]
-    if latent.shape[1] != d:
-        raise ValueError(f"q has {d} elements per head, latent rows {latent.shape[1]}")
-    if q_start.shape[0] != B + 1:
-        raise ValueError(f"q_start has {q_start.shape[0]} entries for {B} sequences")
-    if row_off is not None and tuple(row_off.shape) != (B,):
-        raise ValueError(f"row_off has shape {tuple(row_off.shape)} for {B} sequences")
-    _together(q, latent=latent, q_start=q_start, row_off=row_off, **{lens_name: lens})
-    if out_dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
-    max_q = T if max_q is None else int(max_q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty((T, H, 512), dtype=out_dtype, device=q.device)
-    else:
-        _dev(out, out_dtype, "out", 3)
-        _together(q, out=out)
-        if tuple(out.shape) != (T, H, 512):
-            raise ValueError(f"out has shape {tuple(out.shape)}, not {(T, H, 512)}")
-    lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if want_lse else None
-    return max_q, float(scale), LS_OUT_BF16 if out_dtype == torch.bfloat16 else LS_OUT_F32, out, lse
-
-
-def _span_ws(ws, need, q):
-    if ws is None:
-        return _workspace(need, q.device)
-    _dev(ws, torch.uint8, "ws", 1)
-    _together(q, ws=ws)
-    return ws
+def _span_call(q, latent, q_start, lens, lens_name, row_off, tree_mask, window, align, n_sink, max_q, max_ctx, scale,
+               out_dtype, want_lse, ws, out, stream):
+    """The two span attentions (tree_mask None: the window form)."""
+    with _on(q, stream):
+        dev = q.get_device()
+        qp = _fits(q, torch.bfloat16, 3, dev, "q")
+        kp = _fits(latent, torch.bfloat16, 2, dev, "latent")
+        sp = _fits(q_start, torch.int32, 1, dev, "q_start")
+        lp = _fits(lens, torch.int32, 1, dev, lens_name)
+        T, H, d = q.shape
+        R, d_lat = latent.shape
+        B = lens.shape[0]
+        if d_lat != d:
+            raise ValueError(f"q has {d} elements per head, latent rows {d_lat}")
+        if q_start.shape[0] != B + 1:
+            raise ValueError(f"q_start has {q_start.shape[0]} entries for {B} sequences")
+        op = None
+        if row_off is not None:
+            op = _fits(row_off, torch.int64, 1, dev, "row_off")
+            if row_off.shape[0] != B:
+                raise ValueError(f"row_off has {row_off.shape[0]} entries for {B} sequences")
+        if out_dtype is torch.bfloat16:
+            od = LS_OUT_BF16
+        elif out_dtype is torch.float32:
+            od = LS_OUT_F32
+        else:
+            raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
+        max_q = T if max_q is None else int(max_q)
+        if scale is None:
+            scale = 1.0 / math.sqrt(d)
+        if out is None:
+            out = q.new_empty((T, H, 512), dtype=out_dtype)
+            outp = out.data_ptr()
+        else:
+            outp = _fits(out, out_dtype, 3, dev, "out")
+            if tuple(out.shape) != (T, H, 512):
+                raise ValueError(f"out has shape {tuple(out.shape)}, not {(T, H, 512)}")
+        lse = q.new_empty((T, H), dtype=torch.float32) if want_lse else None
+        lsep = None if lse is None else lse.data_ptr()
+        L = lib()
+        if tree_mask is not None:
+            mp = _fits(tree_mask, torch.int64, 2, dev, "tree_mask")
+            words = tree_mask.shape[1]
+            if tree_mask.shape[0] != T:
+                raise ValueError(f"tree_mask has {tree_mask.shape[0]} rows for {T} tokens")
+        if ws is None:
+            need = (L.ls_window_attention_workspace_size(B, T, H, max_q, window, align, n_sink) if tree_mask is None
+                    else L.ls_tree_attention_workspace_size(B, T, H, max_q, R, max_ctx, window, align, n_sink))
+            if need:
+                ws = q.new_empty((need,), dtype=torch.uint8)
+                wsp, wsn = ws.data_ptr(), need
+            else:
+                wsp, wsn = None, 0
+        else:
+            wsp, wsn = _fits(ws, torch.uint8, 1, dev, "ws"), ws.shape[0]
+        st = _raw_stream(dev)
+        if tree_mask is None:
+            r = L.ls_window_attention(qp, kp, sp, lp, op, B, T, H, d, 512, R, max_q, window, align, n_sink, scale, od,
+                                      outp, lsep, wsp, wsn, st)
+        else:
+            r = L.ls_tree_attention(qp, kp, sp, lp, op, mp, words, B, T, H, d, 512, R, max_q, max_ctx, window, align,
+                                    n_sink, scale, od, outp, lsep, wsp, wsn, st)
+        if r != LS_OK:
+            _check(r)
+    return out, lse
 
 
 def ls_window_attention(q, latent, q_start, kv_len, row_off=None, window: int = 512, align: int = 1,
@@ -732,16 +768,8 @@ def ls_window_attention(q, latent, q_start, kv_len, row_off=None, window: int = 
     p - window + 1) rounded down to a multiple of align (window=1, align=512: the block window of the LSA search).
     max_q: at least the longest sequence's query tokens (default T) -> (out [T,H,512] of out_dtype, lse [T,H] f32 or
     None); out_dtype=torch.float32 is what ls_attention_merge joins with other parts."""
-    with _on(q, stream):
-        max_q, scale, od, out, lse = _span_args(q, latent, q_start, kv_len, row_off, max_q, scale, out_dtype, out,
-                                                want_lse, "kv_len")
-        T, H, d = q.shape
-        B = kv_len.shape[0]
-        ws = _span_ws(ws, lib().ls_window_attention_workspace_size(B, T, H, max_q, window, align, n_sink), q)
-        _check(lib().ls_window_attention(_ptr(q), _ptr(latent), _ptr(q_start), _ptr(kv_len), _ptr(row_off), B, T, H,
-                                         d, 512, latent.shape[0], max_q, window, align, n_sink, scale, od,
-                                         _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream()))
-    return out, lse
+    return _span_call(q, latent, q_start, kv_len, "kv_len", row_off, None, window, align, n_sink, max_q, 0, scale,
+                      out_dtype, want_lse, ws, out, stream)
 
 
 def ls_tree_attention(q, latent, q_start, ctx_len, tree_mask, row_off=None, window: int = 0, align: int = 1,
@@ -755,52 +783,36 @@ def ls_tree_attention(q, latent, q_start, ctx_len, tree_mask, row_off=None, wind
     token t is set when it sees drafted row i of its sequence (its own included).  window > 0 cuts the context as in
     ls_window_attention.  max_ctx: the longest context if the caller knows it (it only decides how the work is
     split) -> (out [T,H,512] of out_dtype, lse [T,H] f32 or None)."""
-    with _on(q, stream):
-        max_q, scale, od, out, lse = _span_args(q, latent, q_start, ctx_len, row_off, max_q, scale, out_dtype, out,
-                                                want_lse, "ctx_len")
-        T, H, d = q.shape
-        B, R = ctx_len.shape[0], latent.shape[0]
-        _dev(tree_mask, torch.int64, "tree_mask", 2)
-        _together(q, tree_mask=tree_mask)
-        if tree_mask.shape[0] != T:
-            raise ValueError(f"tree_mask has {tree_mask.shape[0]} rows for {T} tokens")
-        ws = _span_ws(ws, lib().ls_tree_attention_workspace_size(B, T, H, max_q, R, max_ctx, window, align, n_sink),
-                      q)
-        _check(lib().ls_tree_attention(_ptr(q), _ptr(latent), _ptr(q_start), _ptr(ctx_len), _ptr(row_off),
-                                       _ptr(tree_mask), tree_mask.shape[1], B, T, H, d, 512, R, max_q, max_ctx,
-                                       window, align, n_sink, scale, od, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                       _stream()))
-    return out, lse
+    if tree_mask is None:
+        raise TypeError("tree_mask must be a tensor")
+    return _span_call(q, latent, q_start, ctx_len, "ctx_len", row_off, tree_mask, window, align, n_sink, max_q,
+                      max_ctx, scale, out_dtype, want_lse, ws, out, stream)
 
 
-def _norm_rows(x, name, norm, norm_dim, weight, bias, out, scale, slots):
-    if norm not in LS_NORM:
-        raise ValueError(f"{name}_norm must be one of {sorted(LS_NORM)}, got {norm!r}")
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _dev(t, torch.float32, f"{name}_{what}", 1)
-            if t.shape[0] != norm_dim:
-                raise ValueError(f"{name}_{what} has {t.shape[0]} elements for norm_dim = {norm_dim}")
-            if norm == "none":
-                raise ValueError(f"{name}_{what} without a norm")
-    T, H, d = x.shape
-    p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    return NormRows(p(x), max(x.stride(0), H * d) if T <= 1 else x.stride(0), H, LS_NORM[norm], p(weight), p(bias),
-                    p(out), p(scale), p(slots), 0 if slots is None else out.shape[0])
-
-
-def _head_rows(x, name):
+def _head_rows(x, name, dev):
     """x [T,heads,d] bf16 whose heads lie side by side; a token's rows may be part of a longer row."""
-    if x.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {x.dtype}")
-    if x.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {tuple(x.shape)}")
+    if not (x.dtype is torch.bfloat16 and x.dim() == 3 and x.get_device() == dev):
+        if x.dtype is not torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {x.dtype}")
+        if x.dim() != 3:
+            raise ValueError(f"{name} must have 3 dims, got {tuple(x.shape)}")
+        raise ValueError(f"{name} is on {x.device}, the other tensors on cuda:{dev}")
     T, H, d = x.shape
-    if x.numel() and (x.stride(2) != 1 and d > 1 or (x.stride(1) != d and H > 1) or (T > 1 and x.stride(0) < H * d)):
+    st, sh, sd = x.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1) or (T > 1 and st < H * d):
         raise ValueError(f"{name}: the heads of a token must be contiguous (strides {x.stride()})")
-    return x
+    return x.data_ptr(), (st if T > 1 else H * d), H
+
+
+def _norm_vec(t, norm, norm_dim, dev, name):
+    if t is None:
+        return None
+    p = _fits(t, torch.float32, 1, dev, name)
+    if t.shape[0] != norm_dim:
+        raise ValueError(f"{name} has {t.shape[0]} elements for norm_dim = {norm_dim}")
+    if norm == "none":
+        raise ValueError(f"{name} without a norm")
+    return p
 
 
 def ls_norm_rope(q=None, k=None, pos=None, inv_freq=None, q_norm: str = "none", k_norm: str = "none",
@@ -821,64 +833,77 @@ def ls_norm_rope(q=None, k=None, pos=None, inv_freq=None, q_norm: str = "none", 
     if x is None:
         raise ValueError("ls_norm_rope needs q or k")
     with _on(x, stream):
-        for t, name in ((q, "q"), (k, "k")):
-            if t is not None:
-                _head_rows(t, name)
+        dev = x.get_device()
+        if x.dim() != 3:
+            raise ValueError(f"{'k' if q is None else 'q'} must have 3 dims, got {tuple(x.shape)}")
         T, _, d = x.shape
-        if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d):
-            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree")
-        norm_dim = d if norm_dim is None else int(norm_dim)
-        rope = 0
+        if norm_dim is None:
+            norm_dim = d
+        rope = fp = pp = None
         if inv_freq is not None:
-            _dev(inv_freq, torch.float32, "inv_freq", 1)
-            rope = 2 * inv_freq.shape[0]
+            fp = _fits(inv_freq, torch.float32, 1, dev, "inv_freq")
             if pos is None:
                 raise ValueError("inv_freq without pos")
-            _dev(pos, torch.int64, "pos", 1)
+            pp = _fits(pos, torch.int64, 1, dev, "pos")
             if pos.shape[0] != T:
                 raise ValueError(f"pos has {pos.shape[0]} entries for {T} tokens")
+            rope = 2 * inv_freq.shape[0]
+        if q_norm not in LS_NORM or k_norm not in LS_NORM:
+            raise ValueError(f"q_norm and k_norm must be of {sorted(LS_NORM)}, got {q_norm!r} and {k_norm!r}")
         if fp8 is None:
-            fp8 = k_cache is not None and k_cache.dtype == torch.float8_e4m3fn
+            fp8 = k_cache is not None and k_cache.dtype is torch.float8_e4m3fn
         dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
-        _together(x, q=q, k=k, pos=pos, inv_freq=inv_freq, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight,
-                  k_bias=k_bias, k_cache=k_cache, k_scale=k_scale, slots=slots)
-        if k_cache is None:
-            if slots is not None or k_scale is not None:
-                raise ValueError("slots and k_scale belong to k_cache")
-        else:
-            if k is None:
-                raise ValueError("k_cache without k")
-            if slots is None:
-                raise ValueError("k_cache needs slots")
-            _dev(slots, torch.int64, "slots", 1)
-            if slots.shape[0] != T:
-                raise ValueError(f"slots has {slots.shape[0]} entries for {T} tokens")
-            _dev(k_cache, dt, "k_cache")
-            if tuple(k_cache.shape[1:]) not in ((k.shape[1], d), (d,) if k.shape[1] == 1 else None):
-                raise ValueError(f"k_cache {tuple(k_cache.shape)} does not hold rows of k {tuple(k.shape)}")
-            if fp8:
-                if k_scale is None:
-                    raise ValueError("an fp8 k_cache needs k_scale")
-                _dev(k_scale, torch.float32, "k_scale")
-                if k_scale.numel() != k_cache.shape[0] * k.shape[1]:
-                    raise ValueError(f"k_scale {tuple(k_scale.shape)} does not belong to {tuple(k_cache.shape)}")
-            elif k_scale is not None:
-                raise ValueError("k_scale with a bf16 k_cache")
-        q_out = q_scale = k_out = None
-        rows = [None, None]
+        q_out = q_scale = k_out = qr = kr = None
         if q is not None:
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-            q_scale = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if fp8 else None
-            rows[0] = _norm_rows(q, "q", q_norm, norm_dim, q_weight, q_bias, q_out, q_scale, None)
+            xp, xs, H = _head_rows(q, "q", dev)
+            wp = _norm_vec(q_weight, q_norm, norm_dim, dev, "q_weight")
+            bp = _norm_vec(q_bias, q_norm, norm_dim, dev, "q_bias")
+            q_out = q.new_empty((T, H, d), dtype=dt)
+            if fp8:
+                q_scale = q.new_empty((T, H), dtype=torch.float32)
+            qr = NormRows(xp, xs, H, LS_NORM[q_norm], wp, bp, q_out.data_ptr(), q_scale.data_ptr() if fp8 else None,
+                          None, 0)
         if k is not None:
-            k_out = k_cache
+            xp, xs, H = _head_rows(k, "k", dev)
+            if k.shape[0] != T or k.shape[2] != d:
+                raise ValueError(f"q {tuple(x.shape)} and k {tuple(k.shape)} disagree")
+            wp = _norm_vec(k_weight, k_norm, norm_dim, dev, "k_weight")
+            bp = _norm_vec(k_bias, k_norm, norm_dim, dev, "k_bias")
             if k_cache is None:
-                k_out = torch.empty(k.shape, dtype=dt, device=k.device)
-                k_scale = torch.empty(k.shape[:2], dtype=torch.float32, device=k.device) if fp8 else None
-            rows[1] = _norm_rows(k, "k", k_norm, norm_dim, k_weight, k_bias, k_out, k_scale, slots)
-        _check(lib().ls_norm_rope(*(None if r is None else ctypes.byref(r) for r in rows), _ptr(pos),
-                                  _ptr(inv_freq), T, d, norm_dim, rope, rope_off, int(interleaved), float(eps),
-                                  LS_KEY_FP8_E4M3 if fp8 else LS_KEY_BF16, _stream()))
+                if slots is not None or k_scale is not None:
+                    raise ValueError("slots and k_scale belong to k_cache")
+                k_out = k.new_empty((T, H, d), dtype=dt)
+                op, slp, rows = k_out.data_ptr(), None, 0
+                if fp8:
+                    k_scale = k.new_empty((T, H), dtype=torch.float32)
+                scp = k_scale.data_ptr() if fp8 else None
+            else:
+                if slots is None:
+                    raise ValueError("k_cache needs slots")
+                slp = _fits(slots, torch.int64, 1, dev, "slots")
+                if slots.shape[0] != T:
+                    raise ValueError(f"slots has {slots.shape[0]} entries for {T} tokens")
+                k_out, rows = k_cache, k_cache.shape[0]
+                op = _fits(k_cache, dt, 2 if H == 1 and k_cache.dim() == 2 else 3, dev, "k_cache")
+                if k_cache.shape[-1] != d or (k_cache.dim() == 3 and k_cache.shape[1] != H):
+                    raise ValueError(f"k_cache {tuple(k_cache.shape)} does not hold rows of k {tuple(k.shape)}")
+                scp = None
+                if fp8:
+                    if k_scale is None:
+                        raise ValueError("an fp8 k_cache needs k_scale")
+                    scp = _fits(k_scale, torch.float32, 1 if H == 1 and k_scale.dim() == 1 else 2, dev, "k_scale")
+                    if k_scale.shape[0] != rows or (k_scale.dim() == 2 and k_scale.shape[1] != H):
+                        raise ValueError(f"k_scale {tuple(k_scale.shape)} does not belong to {tuple(k_cache.shape)}")
+                elif k_scale is not None:
+                    raise ValueError("k_scale with a bf16 k_cache")
+            kr = NormRows(xp, xs, H, LS_NORM[k_norm], wp, bp, op, scp, slp, rows)
+        elif k_cache is not None or slots is not None or k_scale is not None:
+            raise ValueError("k_cache, k_scale and slots without k")
+        r = lib().ls_norm_rope(None if qr is None else ctypes.byref(qr), None if kr is None else ctypes.byref(kr), pp,
+                               fp, T, d, norm_dim, rope or 0, rope_off, interleaved, eps,
+                               LS_KEY_FP8_E4M3 if fp8 else LS_KEY_BF16, _raw_stream(dev))
+        if r != LS_OK:
+            _check(r)
     return q_out, q_scale, k_out, k_scale
 
 
