@@ -90,7 +90,9 @@ constexpr size_t kLaOffBars = kLaOffT + kLaTPanels * size_t(kLaPanelBytes);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
-static_assert(kLaQTmem * kLaQPanelBytes <= 2 * kLaVBuf, "the staged query panels fit two value buffers");
+// the query panels on their way to tensor memory take the second and third value buffer
+constexpr size_t kLaOffStage = kLaOffV + kLaVBuf;
+static_assert(kLaQTmem * kLaQPanelBytes == 2 * kLaVBuf, "the staged query panels fit two value buffers");
 // the output's rows on their way out, a 16-byte pad apart (lanes on different banks)
 constexpr int kLaOutPitch16 = 256 * 2 + 16, kLaOutPitch32 = 256 * 4 + 16;
 static_assert(kLaRows * kLaOutPitch32 <= kLaVBufs * kLaVBuf + kLaTPanels * kLaPanelBytes, "output rows fit the ring");
@@ -228,15 +230,6 @@ __device__ __forceinline__ void la_mma_tmem_x4(uint32_t d_tmem, uint32_t a_tmem,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(B_STEP / 16), "n"(2 * B_STEP / 16),
       "n"(3 * B_STEP / 16)
       : "memory");
-}
-
-// Shared-memory row to global memory, asynchronously (sizes and addresses multiples of 16).
-__device__ __forceinline__ void la_bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void la_bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Sets the masked places of 32 logits to -inf; whether one of them (among the
@@ -413,7 +406,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     // ------------------------------------------------------------ copies
     if (lane == 0 && nt > 0) {
       mbar_arrive_expect_tx(&bars->qstage, kLaQTmem * kLaQPanelBytes);
-      la_load_3d(smem + kLaOffV, &M.q4, &bars->qstage, static_cast<int>(grow0), la_v_panel(vh));
+      la_load_3d(smem + kLaOffStage, &M.q4, &bars->qstage, static_cast<int>(grow0), la_v_panel(vh));
       mbar_arrive_expect_tx(&bars->qfull, kLaQSmem * kLaQPanelBytes);
       la_load_3d(smem, &M.q4, &bars->qfull, static_cast<int>(grow0), la_t_panel(vh));
       la_load_3d(smem + 4 * kLaQPanelBytes, &M.q1, &bars->qfull, static_cast<int>(grow0), 8);
@@ -427,11 +420,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         const int box = la_box_rows(cnt);
         const CUtensorMap* four = box == kLaTile ? &M.kv4 : &M.few4;
         const CUtensorMap* one = box == kLaTile ? &M.kv1 : &M.few1;
-        // the value buffers hold the query's staged panels first; the first tile's other panels need not wait
         for (int g = 0; g < 3 && ok; ++g) {
-          const int what = i == 0 ? g : g == 0 ? 2 : g - 1;   // 0, 1: key-only panels; 2: values
+          const int what = g == 0 ? 2 : g - 1;        // 0, 1: key-only panels; 2: values
           if (what == 2) {
-            if (i == 0) ok = mbar_wait(&bars->qtmem, 0, abort_flag);
+            if (i == 1) ok = mbar_wait(&bars->qtmem, 0, abort_flag);   // the staged query panels are read
             if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
             if (!ok) break;
             mbar_arrive_expect_tx(&bars->v_full[vs], 4 * box * 128);
@@ -538,7 +530,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       ok = warp_wait(&bars->qstage, 0, abort_flag);
       for (int p = 0; p < kLaQTmem && ok; ++p) {
         uint32_t w[32];
-        const uint8_t* src = smem + kLaOffV + p * kLaQPanelBytes + r * 128;
+        const uint8_t* src = smem + kLaOffStage + p * kLaQPanelBytes + r * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const uint4 v = *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4));
@@ -678,8 +670,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         else if (P.lse)
           P.lse[row] = v;
       }
-      // rows through shared memory (free now: every copy and MMA of the CTA is done), so that each leaves as
-      // one copy of its 512 or 1024 bytes
+      // rows through shared memory (free now: every copy and MMA of the CTA is done), so that a store covers
+      // a row's 512 bytes (one bulk copy per row took 3000 cycles to issue; this takes 600)
       const bool wide = parts || !P.out_bf16;
       uint8_t* stage = smem + kLaOffV + r * (wide ? kLaOutPitch32 : kLaOutPitch16);
       for (int c = 0; c < 8; ++c) {
@@ -709,16 +701,25 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           }
         }
       }
-      fence_proxy_async_smem();
-      if (live && !(parts && empty)) {                // an empty part is not read
-        const int64_t at = row * kAttnValue + 256 * vh;
-        if (parts)
-          la_bulk_store(P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue + at, stage, 1024);
-        else if (wide)
-          la_bulk_store(static_cast<float*>(P.out) + at, stage, 1024);
-        else
-          la_bulk_store(static_cast<uint16_t*>(P.out) + at, stage, 512);
-        la_bulk_store_wait();
+      __syncwarp();
+      const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
+      uint8_t* dst0 = parts ? reinterpret_cast<uint8_t*>(P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue)
+                            : static_cast<uint8_t*>(P.out);
+      const int size = wide ? 4 : 2;
+      const uint8_t* src0 = smem + kLaOffV + quad * 32 * (wide ? kLaOutPitch32 : kLaOutPitch16) + 16 * lane;
+      dst0 += ((grow0 + quad * 32) * kAttnValue + 256 * vh) * size + 16 * lane;
+#pragma unroll 8
+      for (int rr = 0; rr < 32; ++rr) {               // a warp writes its rows one by one, 512 bytes an access
+        if (!((keep >> rr) & 1u)) continue;
+        if (wide) {
+          const uint4 v = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32);
+          const uint4 w = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32 + 512);
+          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4)) = v;
+          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4) + 512) = w;
+        } else {
+          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 2)) =
+              *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch16);
+        }
       }
       __syncwarp();
     }
