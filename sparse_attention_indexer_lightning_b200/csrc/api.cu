@@ -1708,12 +1708,11 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
   }
   LaMaps maps;
   const uint64_t q_rows = static_cast<uint64_t>(p.T) * p.H, kv_rows = static_cast<uint64_t>(p.n_rows);
-  ls_status s = make_panel_map(&maps.q4, p.q, q_rows, kLaRows, 4);
-  if (s == LS_OK) s = make_panel_map(&maps.q1, p.q, q_rows, kLaRows, 1);
-  if (s == LS_OK) s = make_panel_map(&maps.kv4, latent, kv_rows, kLaTile, 4);
-  if (s == LS_OK) s = make_panel_map(&maps.kv1, latent, kv_rows, kLaTile, 1);
-  if (s == LS_OK) s = make_panel_map(&maps.few4, latent, kv_rows, 16, 4);
-  if (s == LS_OK) s = make_panel_map(&maps.few1, latent, kv_rows, 16, 1);
+  ls_status s = make_panel_map(&maps.q, p.q, q_rows, kLaHalf, kLaKPer);
+  if (s == LS_OK) s = make_panel_map(&maps.k, latent, kv_rows, kLaHalf, kLaKPer);
+  if (s == LS_OK) s = make_panel_map(&maps.v, latent, kv_rows, kLaTile, 2);
+  if (s == LS_OK) s = make_panel_map(&maps.k_few, latent, kv_rows, kLaFew / 2, kLaKPer);
+  if (s == LS_OK) s = make_panel_map(&maps.v_few, latent, kv_rows, kLaFew, 2);
   if (s != LS_OK) return s;
   {
     ProfScope prof("latent_attn_kernel", st);

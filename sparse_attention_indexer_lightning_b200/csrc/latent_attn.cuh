@@ -10,40 +10,47 @@
 //
 // The query heads of a sequence's tokens are consecutive rows of q, so 128 of
 // them (whatever the number of heads) are the M of every MMA.  One pass over
-// the rows any of them sees, in tiles of 64, with the running maximum and sum
-// of the softmax:
+// the rows any of them sees, in tiles of 128, with the running maximum and sum
+// of the softmax.
 //
-//  - tensor memory holds 512 columns, and an fp32 output of 512 value columns
-//    would take all of them; a CTA therefore keeps half of the value columns
-//    (256) and two CTAs work on the same 128 query rows, each computing the
-//    logits;
-//  - of the query's nine 64-element panels the four of this CTA's value half
-//    live in tensor memory as the MMAs' A operand and five in shared memory
-//    (80 KB); a tile's value panels stay until its output is accumulated
-//    (three tiles of them, 96 KB); the other five have one place each (40 KB),
-//    free for the next tile as soon as the logits passed them.  A copy takes
-//    four panels at once (a 3-D box of 64 elements x rows x panels): with one
-//    panel a copy the issue alone took 2000 of a tile's 3200 cycles.  The logits
-//    take the value panels first, so both kinds of copies run about 1500
-//    cycles ahead.  A value panel is staged once: the logits read it as
-//    K-major keys and the output as MN-major values (the same bytes);
+// Two CTAs of a cluster share the 128 query rows (tcgen05 cta_group::2, M =
+// 128): CTA c holds query rows 64c .. 64c + 63, their logits and their fp32
+// output of all 512 value columns.  An accumulator of 64 rows x N columns lies
+// in 128 lanes x N / 2 tensor-memory columns (lane r and lane r + 64 hold row
+// r's first and second half), so the output takes 256 of the 512 columns and
+// two tiles' logits 128.  (One CTA with all 128 rows would need all 512 for
+// its output, and two CTAs with half of the value columns each would both
+// compute the logits: 1664 against 1088 multiply-adds per query row and cache
+// row; that form took 2600 cycles per 64 rows, this one needs 2180 per 128.)
+// Per tile each CTA stages
+//  - half of the rows as keys (64 x 576, 72 KB, in three groups of three
+//    panels that are free again as soon as the logits passed them),
+//  - half of the value columns of all rows (128 x 256, 64 KB, in two groups,
+//    one per output MMA of N = 256),
+// and the tensor core of each reads both CTAs' halves.  72 KB of query rows
+// and 16 KB of weights fill the shared memory.
+//
+//  - the first CTA of the pair issues all MMAs; both CTAs' copies report to
+//    its barriers;
 //  - the logits of tile i + 1 are issued before the output of tile i, so the
-//    softmax of a tile runs beside the MMAs of the next;
-//  - the weights go back to tensor memory as bf16 (A operand of the output);
-//    the output is rescaled only when a row's maximum grew by more than 16
+//    softmax of a tile runs beside the MMAs of its neighbours;
+//  - a row's logits of a tile lie in two lanes, so two threads share a row
+//    and exchange its maximum; the weights go to shared memory as bf16;
+//  - the output is rescaled only when a row's maximum grew by more than 16
 //    (in log2 units: weights stay below 2^16, which neither bf16 nor fp32
 //    holds less exactly than weights below 1); the sinks, a few rows, come
 //    after the window, so that the first reference is the maximum of many.
 //
-// Rounding to fewer bits: the weights (bf16, half a step is 2^-8 of a weight; the sum that
-// divides the output is that of the rounded weights, so they still sum to 1)
-// and the output when it is asked for in bf16.  Logits, sums, lse are fp32.
+// Rounding to fewer bits: the weights (bf16, half a step is 2^-8 of a weight;
+// the sum that divides the output is that of the rounded weights, so they
+// still sum to 1) and the output when it is asked for in bf16.  Logits, sums,
+// lse are fp32.
 //
 // Masked places weigh exactly 0 whatever they hold: a tile that not every row
-// sees whole is checked for logits that are not finite at masked places, and
-// only then the staged values are searched for elements that are not finite
-// (a weight of 0 times one of them would be NaN) and cleared.  A visible row
-// with a NaN or +inf logit makes its own query row NaN, and no other.
+// sees whole is checked for logits that are not finite, and only then the
+// staged values are searched for elements that are not finite (a weight of 0
+// times one of them would be NaN) and cleared.  A visible row with a NaN or
+// +inf logit makes its own query row NaN, and no other.
 //
 // Few query rows over a long span: the tiles are split over n_split CTA pairs,
 // each writing its part (fp32, with its lse) to the workspace, and
@@ -56,46 +63,42 @@
 
 namespace lsi {
 
-constexpr int kLaRows = 128;                          // query rows per CTA: the MMA's M
-constexpr int kLaTile = 64;                           // cache rows per tile
-constexpr int kLaPanelBytes = kLaTile * 128;          // 8 KB: 64 elements of 64 rows
-constexpr int kLaVPanels = 4;                         // value panels of a CTA's half
-constexpr int kLaTPanels = 5;                         // panels only the logits read
-constexpr int kLaQTmem = 4;                           // query panels in tensor memory
-constexpr int kLaQSmem = 5;                           // query panels in shared memory
-constexpr int kLaQPanelBytes = kLaRows * 128;         // 16 KB
-constexpr int kLaVBuf = kLaVPanels * kLaPanelBytes;  // 32 KB: the value panels of a tile
-constexpr int kLaVBufs = 3;
-constexpr int kLaTFirst = 4;                          // key-only panels freed by a commit of their own
-constexpr int kLaThreads = 6 * 32;                    // copies, MMA, 4 softmax / epilogue warps
-constexpr int kLaColO = 0, kLaColS = 256, kLaColQ = 384;            // tensor-memory columns
+constexpr int kLaRows = 128;                          // query rows of a CTA pair: the MMAs' M
+constexpr int kLaHalf = 64;                           // ... of a CTA
+constexpr int kLaTile = 128;                          // cache rows per tile
+constexpr int kLaFew = 32;                            // a tile of at most so many rows is staged as so many
+constexpr int kLaPanels = kAttnLatent / 64;           // 9 panels of 64 elements
+constexpr int kLaKGroups = 3, kLaKPer = 3;            // the key panels' groups
+constexpr int kLaPanelBytes = kLaHalf * 128;          // 8 KB: 64 elements of 64 rows
+constexpr int kLaVGroup = 2 * kLaTile * 128;          // 32 KB: two value panels of 128 rows
+constexpr int kLaThreads = 6 * 32;                    // copies, MMA (first CTA), 4 softmax / epilogue warps
+constexpr int kLaColO = 0, kLaColS = 256;             // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
 constexpr int kLaMaxSplit = 64;
 
 struct LaBars {
-  uint64_t qfull, qstage, qtmem;     // query: shared-memory panels landed; staged ones landed; in tensor memory
-  uint64_t t_full;                   // a tile's key-only panels have landed (two arrivals)
-  uint64_t t_empty[2];               // the first four, the last one are read
-  uint64_t v_full[kLaVBufs], v_empty[kLaVBufs];
+  uint64_t qfull, k_full, v_full[2]; // first CTA: both CTAs' query rows, keys of a tile, value groups have landed
+  uint64_t k_empty[3], v_empty[2];   // key groups, value groups are read
+  uint64_t v_seen;                   // a tile's values have landed in both CTAs (told by the first one's MMA warp)
   uint64_t sfull[2];                 // logits in tensor memory
-  uint64_t pfull[2];                 // weights in tensor memory
+  uint64_t pfull;                    // first CTA: both CTAs' weights in shared memory (8 warps)
   uint64_t odone;                    // output MMAs of a tile are complete
+  uint64_t mx[2];                    // the two warps that share 32 rows have written their maxima
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kLaOffV = size_t(kLaQSmem) * kLaQPanelBytes;
-constexpr size_t kLaOffT = kLaOffV + kLaVBufs * size_t(kLaVBuf);
-constexpr size_t kLaOffBars = kLaOffT + kLaTPanels * size_t(kLaPanelBytes);
+constexpr size_t kLaOffK = size_t(kLaPanels) * kLaPanelBytes;               // behind the query rows
+constexpr size_t kLaOffV = kLaOffK + size_t(kLaPanels) * kLaPanelBytes;
+constexpr size_t kLaOffP = kLaOffV + 2 * size_t(kLaVGroup);
+constexpr size_t kLaOffX = kLaOffP + 2 * size_t(kLaPanelBytes);             // exchanged maxima / sums: 2 x 128 floats
+constexpr size_t kLaOffBars = kLaOffX + 2 * 128 * sizeof(float);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
-// the query panels on their way to tensor memory take the second and third value buffer
-constexpr size_t kLaOffStage = kLaOffV + kLaVBuf;
-static_assert(kLaQTmem * kLaQPanelBytes == 2 * kLaVBuf, "the staged query panels fit two value buffers");
 // the output's rows on their way out, a 16-byte pad apart (lanes on different banks)
-constexpr int kLaOutPitch16 = 256 * 2 + 16, kLaOutPitch32 = 256 * 4 + 16;
-static_assert(kLaRows * kLaOutPitch32 <= kLaVBufs * kLaVBuf + kLaTPanels * kLaPanelBytes, "output rows fit the ring");
+constexpr int kLaOutPitch16 = kAttnValue * 2 + 16, kLaOutPitch32 = kAttnValue * 4 + 16;
+static_assert(kLaHalf * kLaOutPitch32 <= kLaOffP - kLaOffK, "output rows fit the staged keys and values");
 
 struct LatentAttnParams {
   const uint16_t* q = nullptr;        // [T * H][576]
@@ -128,7 +131,7 @@ __device__ __forceinline__ uint64_t la_low_mask(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
-// The rows that a tile of query rows can see, cut into tiles of 64.
+// The rows that a tile of query rows can see, cut into tiles of 128.
 struct LaSpan {
   int sink_len;          // rows [0, sink_len): sinks apart from the window
   int lo, hi;            // window / context rows
@@ -154,22 +157,18 @@ struct LaSpan {
   }
 };
 
-// First of the four value panels of a CTA of value half vh, first of the four that it only reads as keys besides
-// panel 8 (rotary): half 0 has the values of panels 0-3, half 1 those of panels 4-7.
-__device__ __forceinline__ int la_v_panel(int vh) { return 4 * vh; }
-__device__ __forceinline__ int la_t_panel(int vh) { return 4 - 4 * vh; }
-
-// Box of 64 elements x rows x panels: x in elements of a panel, y the row, z the panel.
-__device__ __forceinline__ void la_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int y, int z) {
+// Box of 64 elements x rows x panels (y the row, z the panel) into this CTA's shared memory, reported to a barrier
+// of the pair (a cluster address).
+__device__ __forceinline__ void la_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(z)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
       : "memory");
 }
 
-// Rows of a tile as they are staged: 64, or 16 for a tile of at most 16 (panels lie that many rows apart).
-__device__ __forceinline__ int la_box_rows(int cnt) { return cnt <= 16 ? 16 : kLaTile; }
+// Rows of a tile as it is staged.
+__device__ __forceinline__ int la_box_rows(int cnt) { return cnt <= kLaFew ? kLaFew : kLaTile; }
 
 // Warp-uniform bounded wait in which every lane tests the barrier: when the
 // phase is complete already, the common case of the MMA warp, it costs one
@@ -177,6 +176,21 @@ __device__ __forceinline__ int la_box_rows(int cnt) { return cnt <= 16 ? 16 : kL
 __device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return warp_wait(bar, parity, abort_flag);
+}
+
+// Address of this CTA's shared-memory object in CTA `rank` of the cluster, and an arrival there.  What the arrival
+// tells of (copies that have landed, weights behind a proxy fence) is read by the tensor cores alone, so it takes no
+// release over the cluster: that, and an acquire fence at the other end, cost 1000 cycles each (10000 cycles a tile).
+__device__ __forceinline__ uint32_t la_map(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void la_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void la_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 2^x: the hardware's approximation (relative error 2^-22; 0 below 2^-126).
@@ -196,50 +210,37 @@ __device__ __forceinline__ float la_sum2(uint64_t v) {
   return a + b;
 }
 
-// Four MMAs along one 64-element panel (K = 16 each): one election, the
-// descriptors stepped by 32 bytes.  A in shared memory (a_desc) ...
-__device__ __forceinline__ void la_mma_panel(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// One MMA of the CTA pair (K = 16), issued by a converged warp through one elected lane.
+__device__ __forceinline__ void la_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
-      "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// ... and A in tensor memory (8 columns a step), B stepped by b_step.
-template <int B_STEP>
-__device__ __forceinline__ void la_mma_tmem_x4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
+
+// The barrier at bar's place receives an arrival once the MMAs issued so far are done, in the CTAs of the mask (by
+// default both).
+__device__ __forceinline__ void la_commit_both(uint64_t* bar, uint16_t mask = 3) {
   asm volatile(
-      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(B_STEP / 16), "n"(2 * B_STEP / 16),
-      "n"(3 * B_STEP / 16)
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
       : "memory");
 }
 
-// Sets the masked places of 32 logits to -inf; whether one of them (among the
-// places `there` that the MMAs wrote) was not finite.
+// Sets the masked places of 32 logits to -inf; whether one of the places
+// `there` that the MMAs wrote was not finite.
 __device__ __forceinline__ bool la_mask_row(uint32_t (&v)[32], uint32_t vis, uint32_t there) {
-  const uint32_t hidden = there & ~vis;
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    if (hidden & (1u << j)) bad |= (v[j] & 0x7f800000u) == 0x7f800000u;
+    if (there & (1u << j)) bad |= (v[j] & 0x7f800000u) == 0x7f800000u;
     if (!(vis & (1u << j))) v[j] = 0xff800000u;
   }
   return bad;
@@ -289,24 +290,26 @@ __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const u
 
 // Tensor maps over rows of 9 panels of 64 elements, boxes of 64 elements x rows x panels, 128-byte swizzle.
 struct LaMaps {
-  CUtensorMap q4, q1;       // q rows: 128 x 4 panels, 128 x 1
-  CUtensorMap kv4, kv1;     // latent rows: 64 x 4, 64 x 1
-  CUtensorMap few4, few1;   // latent rows: 16 x 4, 16 x 1
+  CUtensorMap q;            // q rows: 64 x 3 panels
+  CUtensorMap k, v;         // latent rows: 64 x 3, 128 x 2
+  CUtensorMap k_few, v_few; // latent rows: 16 x 3, 32 x 2
 };
 
-// grid: B * max_tiles * n_split * 2 CTAs, the value half innermost.
-__global__ void __launch_bounds__(kLaThreads, 1)
+// grid: B * max_tiles * n_split pairs of CTAs.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
   extern __shared__ uint8_t la_raw[];
   uint8_t* smem = smem_align1024(la_raw);
   LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
   volatile int* abort_flag = &bars->abort_flag;
-  const int warp = threadIdx.x >> 5;
+  // (broadcasts of what is the same in a warp anyway let the compiler keep it, and the MMAs' operands, uniform: an
+  // MMA whose operands move from a lane's registers takes 48 cycles to issue)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
 
-  // ------------------------------------------------------------ this CTA's work
+  // ------------------------------------------------------------ this pair's work (the same in both CTAs)
   int64_t bid = blockIdx.x;
-  const int vh = static_cast<int>(bid & 1);
+  const int cr = static_cast<int>(bid & 1);           // rank in the pair
   bid >>= 1;
   const int split = static_cast<int>(bid % P.n_split);
   bid /= P.n_split;
@@ -365,187 +368,185 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int per = (all + P.n_split - 1) / P.n_split;
   const int i0 = split * per < all ? split * per : all;
   const int i1 = i0 + per < all ? i0 + per : all;
-  const int nt = i1 - i0;
+  const int nt = __shfl_sync(0xffffffffu, i1 - i0, 0);
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->qfull, 1);
-    mbar_init(&bars->qstage, 1);
-    mbar_init(&bars->qtmem, 4);
-    mbar_init(&bars->t_full, 2);
-    mbar_init(&bars->t_empty[0], 1);
-    mbar_init(&bars->t_empty[1], 1);
-    for (int i = 0; i < kLaVBufs; ++i) {
-      mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 1);
+    mbar_init(&bars->k_full, kLaKGroups);
+    for (int g = 0; g < kLaKGroups; ++g) mbar_init(&bars->k_empty[g], 1);
+    mbar_init(&bars->v_seen, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bars->v_full[g], 1);
+      mbar_init(&bars->v_empty[g], 1);
+      mbar_init(&bars->sfull[g], 1);
+      mbar_init(&bars->mx[g], 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->pfull[i], 4);
-    }
+    mbar_init(&bars->pfull, 8);
     mbar_init(&bars->odone, 1);
     mbar_init(&bars->drain, 1);
     bars->abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&bars->tmem_base, 512);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars->tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&M.q4);
-    tma_prefetch_desc(&M.q1);
-    tma_prefetch_desc(&M.kv4);
-    tma_prefetch_desc(&M.kv1);
+    tma_prefetch_desc(&M.q);
+    tma_prefetch_desc(&M.k);
+    tma_prefetch_desc(&M.v);
   }
   tc_fence_before();
   __syncthreads();
+  la_cluster_sync();                                  // both CTAs' barriers stand before anyone arrives on them
   tc_fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
+    // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).
     if (lane == 0 && nt > 0) {
-      mbar_arrive_expect_tx(&bars->qstage, kLaQTmem * kLaQPanelBytes);
-      la_load_3d(smem + kLaOffStage, &M.q4, &bars->qstage, static_cast<int>(grow0), la_v_panel(vh));
-      mbar_arrive_expect_tx(&bars->qfull, kLaQSmem * kLaQPanelBytes);
-      la_load_3d(smem, &M.q4, &bars->qfull, static_cast<int>(grow0), la_t_panel(vh));
-      la_load_3d(smem + 4 * kLaQPanelBytes, &M.q1, &bars->qfull, static_cast<int>(grow0), 8);
+      const bool first = cr == 0;
+      const uint32_t qfull = la_map(&bars->qfull, 0), k_full = la_map(&bars->k_full, 0);
+      if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
+      for (int g = 0; g < kLaKGroups; ++g)
+        la_load_3d(smem + g * kLaKPer * kLaPanelBytes, &M.q, qfull, static_cast<int>(grow0 + kLaHalf * cr),
+                   kLaKPer * g);
       bool ok = true;
-      int nT = 0, nV = 0;                             // arrivals on t_full, value buffers filled
-      int vs = 0, vph = 1;                            // value buffer and the parity that says it is free
-      for (int i = 0; i < nt && ok; ++i) {
-        int kind, a, cnt;
-        sp.tile(i0 + i, kind, a, cnt);
-        const int row = static_cast<int>(off + a + (kind ? kv : 0));
-        const int box = la_box_rows(cnt);
-        const CUtensorMap* four = box == kLaTile ? &M.kv4 : &M.few4;
-        const CUtensorMap* one = box == kLaTile ? &M.kv1 : &M.few1;
-        for (int g = 0; g < 3 && ok; ++g) {
-          const int what = g == 0 ? 2 : g - 1;        // 0, 1: key-only panels; 2: values
-          if (what == 2) {
-            if (i == 1) ok = mbar_wait(&bars->qtmem, 0, abort_flag);   // the staged query panels are read
-            if (ok) ok = mbar_wait(&bars->v_empty[vs], vph, abort_flag);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&bars->v_full[vs], 4 * box * 128);
-            la_load_3d(smem + kLaOffV + vs * kLaVBuf, four, &bars->v_full[vs], row, la_v_panel(vh));
-            ++nV;
-            if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
-          } else {
-            ok = mbar_wait(&bars->t_empty[what], (i & 1) ^ 1, abort_flag);
-            if (!ok) break;
-            uint8_t* dst = smem + kLaOffT;
-            mbar_arrive_expect_tx(&bars->t_full, (what ? 1 : 4) * box * 128);
-            if (what == 0)
-              la_load_3d(dst, four, &bars->t_full, row, la_t_panel(vh));
-            else
-              la_load_3d(dst + kLaTFirst * box * 128, one, &bars->t_full, row, 8);
-            ++nT;
+      // keys of tile i, then values of tile i - 1: the order in which their places become free
+      for (int i = 0; i <= nt && ok; ++i) {
+        if (i < nt) {
+          int kind, a, cnt;
+          sp.tile(i0 + i, kind, a, cnt);
+          const int box = la_box_rows(cnt) / 2;       // this CTA's half of the rows
+          const int row = static_cast<int>(off + a + (kind ? kv : 0)) + box * cr;
+          for (int g = 0; g < kLaKGroups; ++g) {
+            if (!mbar_wait(&bars->k_empty[g], (i & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (first) mbar_arrive_expect_tx(&bars->k_full, 2 * kLaKPer * box * 128);
+            la_load_3d(smem + kLaOffK + g * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full, row,
+                       kLaKPer * g);
+          }
+        }
+        if (i > 0 && ok) {
+          const int j = i - 1;
+          int kind, a, cnt;
+          sp.tile(i0 + j, kind, a, cnt);
+          const int box = la_box_rows(cnt);
+          const int row = static_cast<int>(off + a + (kind ? kv : 0));
+          for (int g = 0; g < 2; ++g) {
+            // output MMA g has value columns 256 g .. : this CTA's 128 of them are panels 4 g + 2 cr and the next
+            if (!mbar_wait(&bars->v_empty[g], (j & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (first) mbar_arrive_expect_tx(&bars->v_full[g], 2 * 2 * box * 128);
+            la_load_3d(smem + kLaOffV + g * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, la_map(&bars->v_full[g], 0),
+                       row, 4 * g + 2 * cr);
           }
         }
       }
-      // no copy is in flight when the CTA ends (matters after an abort only; a tile whose second half was never
-      // asked for cannot complete its phase, so its first half is given the second's arrival)
-      mbar_wait_drain(&bars->qstage, 0);
-      mbar_wait_drain(&bars->qfull, 0);
-      if (nT & 1) mbar_arrive(&bars->t_full);
-      if (nT > 0) mbar_wait_drain(&bars->t_full, ((nT - 1) >> 1) & 1);
-      for (int k = nV > kLaVBufs ? nV - kLaVBufs : 0; k < nV; ++k)
-        mbar_wait_drain(&bars->v_full[k % kLaVBufs], (k / kLaVBufs) & 1);
+      if (!ok) {
+        // after an abort: the copies in flight (microseconds) land before the CTA ends
+        const uint64_t t = globaltimer_ns();
+        while (globaltimer_ns() - t < 1000000ull) __nanosleep(1000);
+      }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer of the pair (first CTA)
     const uint32_t base = smem_u32(smem);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, kLaVPanels * 64) | (1u << 16);   // B MN-major
-    bool ok = nt > 0;
-    if (ok) ok = warp_wait(&bars->qtmem, 0, abort_flag);
-    if (ok) ok = warp_wait(&bars->qfull, 0, abort_flag);
-    tc_fence_after();
-    int n16_prev = 0;
-    int vs = 0, vph = 0, vprev = 0;
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, 256) | (1u << 16);   // B MN-major
+    bool ok = nt > 0 && cr == 0;
+    if (ok) ok = la_wait_all(&bars->qfull, 0, abort_flag);
+    const uint64_t qdesc = sw128_kmajor_desc(base), kdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffK)),
+                   pdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffP)),
+                   vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
+                   vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
+    const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
+    bool full_prev = false;
     for (int i = 0; i <= nt && ok; ++i) {
-      int n16 = 0;
-      const int vcur = vs;
+      bool full = false;
       if (i < nt) {
-        const int st = i & 1;
         int kind, a, cnt;
         sp.tile(i0 + i, kind, a, cnt);
-        n16 = (cnt + 15) >> 4;
-        const uint32_t idesc_s = idesc_bf16_f32(kLaRows, 16 * n16);
-        const uint32_t d = tmem + kLaColS + 64 * st;
-        const uint32_t pitch = la_box_rows(cnt) * 128;   // bytes between panels
-        if (!la_wait_all(&bars->v_full[vs], vph, abort_flag)) { ok = false; break; }
+        full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
+        const uint32_t d = tmem + kLaColS + 64 * (i & 1);
+        if (!la_wait_all(&bars->k_full, i & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vs * kLaVBuf;
+        // the two sizes apart, so that every descriptor is a constant away from one of two
+        if (full) {
 #pragma unroll
-        for (int p = 0; p < kLaVPanels; ++p)
-          la_mma_tmem_x4<32>(d, tmem + kLaColQ + 32 * p, sw128_kmajor_desc(vb + p * pitch), idesc_s,
-                             p ? 1u : 0u);
-        if (!la_wait_all(&bars->t_full, i & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
+          for (int p = 0; p < kLaPanels; ++p) {
 #pragma unroll
-        for (int p = 0; p < kLaTPanels; ++p) {
-          la_mma_panel(d, sw128_kmajor_desc(base + p * kLaQPanelBytes),
-                       sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffT) + p * pitch), idesc_s, 1u);
-          if (p == kLaTFirst - 1) umma_commit_warp(&bars->t_empty[0]);
+            for (int kk = 0; kk < 4; ++kk)
+              la_mma(d, qdesc + (p * kLaPanelBytes + 32 * kk) / 16, kdesc + (p * kLaPanelBytes + 32 * kk) / 16,
+                     idesc_bf16_f32(kLaRows, kLaTile), (p | kk) ? 1u : 0u);
+            if (p % kLaKPer == kLaKPer - 1) la_commit_both(&bars->k_empty[p / kLaKPer]);
+          }
+        } else {
+          // few rows: a group's panels lie 16 rows apart
+#pragma unroll
+          for (int p = 0; p < kLaPanels; ++p) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              la_mma(d, qdesc + (p * kLaPanelBytes + 32 * kk) / 16,
+                     kdesc + (p / kLaKPer * kLaKPer * kLaPanelBytes + p % kLaKPer * (kLaFew * 64) + 32 * kk) / 16,
+                     idesc_bf16_f32(kLaRows, kLaFew), (p | kk) ? 1u : 0u);
+            if (p % kLaKPer == kLaKPer - 1) la_commit_both(&bars->k_empty[p / kLaKPer]);
+          }
         }
-        umma_commit_warp(&bars->sfull[st]);
-        umma_commit_warp(&bars->t_empty[1]);
-        if (++vs == kLaVBufs) { vs = 0; vph ^= 1; }
+        la_commit_both(&bars->sfull[i & 1]);
       }
       if (i > 0) {                                    // the output of the tile before
-        const int j = i - 1, st = j & 1;
-        if (!la_wait_all(&bars->pfull[st], (j >> 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t vb = base + static_cast<uint32_t>(kLaOffV) + vprev * kLaVBuf;
-        const uint32_t a_tmem = tmem + kLaColS + 64 * st;
-        const uint64_t bdesc = sw128_mnmajor_desc(vb, n16_prev == 1 ? 16 * 128 : kLaPanelBytes);
-        if (n16_prev == 4) {
-          la_mma_tmem_x4<2048>(tmem + kLaColO, a_tmem, bdesc, idesc_o, j ? 1u : 0u);
-        } else {
-          for (int s = 0; s < n16_prev; ++s)
-            umma_f16_tmem_a_warp(tmem + kLaColO, a_tmem + 8 * s, bdesc + s * (2048 / 16), idesc_o, (j | s) ? 1u : 0u);
+        const int j = i - 1;
+        if (!la_wait_all(&bars->v_full[0], j & 1, abort_flag) || !la_wait_all(&bars->v_full[1], j & 1, abort_flag)) {
+          ok = false;
+          break;
         }
-        umma_commit_warp(&bars->v_empty[vprev]);
-        umma_commit_warp(&bars->odone);
+        if (lane == 0) {
+          la_arrive_at(seen0);
+          la_arrive_at(seen1);
+        }
+        __syncwarp();
+        if (!la_wait_all(&bars->pfull, j & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t acc0 = j ? 1u : 0u;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t d = tmem + kLaColO + 128 * g;
+          if (full_prev) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vdesc + (g * kLaVGroup + 2048 * s) / 16,
+                     idesc_o, s ? 1u : acc0);
+          } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              la_mma(d, pdesc + 32 * s / 16, vdesc_few + (g * kLaVGroup + 2048 * s) / 16, idesc_o, s ? 1u : acc0);
+          }
+          la_commit_both(&bars->v_empty[g]);
+        }
+        la_commit_both(&bars->odone);
       }
-      n16_prev = n16;
-      vprev = vcur;
+      full_prev = full;
     }
     // all MMAs this warp started are complete once `drain` flips
-    if (nt > 0) {
-      umma_commit_warp(&bars->drain);
+    if (nt > 0 && cr == 0) {
+      la_commit_both(&bars->drain, 1);
       if (lane == 0) mbar_wait_drain(&bars->drain, 0);
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
     const int quad = warp & 3;                        // warps 2-5: tensor-memory lanes 32 * (warp & 3) ..
-    const int r = quad * 32 + lane;
+    const int tl = quad * 32 + lane;                  // tensor-memory lane
+    const int r = tl & 63, half = tl >> 6;            // row of this CTA, and which half of a tile's rows
+    const int grp = quad & 1;                         // the two warps that share 32 rows
+    const int rq = kLaHalf * cr + r;                  // row of the pair
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const bool live = r < nrows;
-    const int tok = static_cast<int>((r0 + (live ? r : nrows - 1)) / H);
+    const bool live = rq < nrows;
+    const int tok = static_cast<int>((r0 + (live ? rq : nrows - 1)) / H);
+    float* xch = reinterpret_cast<float*>(smem + kLaOffX);
+    const uint32_t pfull0 = la_map(&bars->pfull, 0);
     bool ok = true;
-    if (nt > 0) {
-      // the staged query panels of this row into tensor memory
-      ok = warp_wait(&bars->qstage, 0, abort_flag);
-      for (int p = 0; p < kLaQTmem && ok; ++p) {
-        uint32_t w[32];
-        const uint8_t* src = smem + kLaOffStage + p * kLaQPanelBytes + r * 128;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + ((c ^ (r & 7)) << 4));
-          w[4 * c] = v.x;
-          w[4 * c + 1] = v.y;
-          w[4 * c + 2] = v.z;
-          w[4 * c + 3] = v.w;
-        }
-        tmem_st_32x32(trow + kLaColQ + 32 * p, w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->qtmem);
-    }
     // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
     int hi, lo;
     const uint64_t* branch = nullptr;
@@ -567,19 +568,22 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const bool turn = P.scale < 0.f;
     const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
     float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
-    int vs = 0;
     for (int i = 0; i < nt && ok; ++i) {
       const int st = i & 1;
-      int kind, a, cnt;
-      sp.tile(i0 + i, kind, a, cnt);
-      const bool whole = kind == 0 && cnt == kLaTile && a + kLaTile <= sp.hi_min &&
-                         (a + kLaTile <= P.n_sink || a >= sp.lo_max);
+      int kind, a0, cnt0;
+      sp.tile(i0 + i, kind, a0, cnt0);
+      const bool whole = kind == 0 && cnt0 == kLaTile && a0 + kLaTile <= sp.hi_min &&
+                         (a0 + kLaTile <= P.n_sink || a0 >= sp.lo_max);
+      // this thread's rows of the tile: `hs` from a on, cnt of them in the tile
+      const int hs = la_box_rows(cnt0) / 2;
+      const int a = a0 + hs * half;
+      const int left = cnt0 - hs * half, cnt = left < 0 ? 0 : left < hs ? left : hs;
       uint64_t vis = ~0ull;
       if (!whole) {
         if (kind == 0)
           vis = la_low_mask(hi - a < cnt ? hi - a : cnt) & (la_low_mask(P.n_sink - a) | ~la_low_mask(lo - a));
         else
-          vis = __ldg(branch + (a >> 6)) & la_low_mask(cnt);
+          vis = cnt > 0 ? (__ldg(branch + (a >> 6)) >> (a & 63)) & la_low_mask(cnt) : 0ull;
       }
       if (!warp_wait(&bars->sfull[st], (i >> 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
@@ -597,38 +601,56 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       if (!whole) {
-        const uint64_t there = la_low_mask(16 * ((cnt + 15) >> 4));
+        const uint64_t there = la_low_mask(hs);
         const bool bad = la_mask_row(va, static_cast<uint32_t>(vis), static_cast<uint32_t>(there)) |
                          la_mask_row(vb, static_cast<uint32_t>(vis >> 32), static_cast<uint32_t>(there >> 32));
-        // A row that holds something not finite gives every query row a logit that is not finite, so each
-        // warp finds out for its own query rows, and clears the staged values before its own arrival (two
-        // warps that clear the same piece store the same bytes).
+        // A cache row that holds something not finite gives every query row of the pair a logit that is not
+        // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
+        // arrival (two warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
-          uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + vs * kLaVBuf);
-          for (int e = lane; e < kLaVPanels * 8 * la_box_rows(cnt); e += 32) {
-            uint4* at = v4 + e;
-            uint4 x = *at;
-            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((xw[k] & 0x7f80u) == 0x7f80u) xw[k] &= 0xffff0000u;
-              if ((xw[k] & 0x7f800000u) == 0x7f800000u) xw[k] &= 0x0000ffffu;
-            }
-            *at = x;
+          if ((i > 0 && !warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) ||
+              !warp_wait(&bars->v_seen, i & 1, abort_flag)) {
+            ok = false;
+            break;
           }
-          fence_proxy_async_smem();
+          for (int g = 0; g < 2; ++g) {
+            uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + g * kLaVGroup);
+            for (int e = lane; e < 2 * 8 * 2 * hs; e += 32) {
+              uint4 x = v4[e];
+              uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((xw[k] & 0x7f80u) == 0x7f80u) xw[k] &= 0xffff0000u;
+                if ((xw[k] & 0x7f800000u) == 0x7f800000u) xw[k] &= 0x0000ffffu;
+              }
+              v4[e] = x;
+            }
+          }
         }
       }
-      const float mt = la_row_max(va, vb, sl2);
+      // the row's maximum: this thread's half and, from the other warp of the pair, the other half
+      float mt = la_row_max(va, vb, sl2);
+      xch[128 * st + tl] = mt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->mx[grp]);
+      if (!warp_wait(&bars->mx[grp], i & 1, abort_flag)) { ok = false; break; }
+      mt = fmaxf(mt, xch[128 * st + (tl ^ 64)]);
       const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
-      if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
-        if (grow) m = mt;
-        l *= f;
-        lt *= f;
-        if (i > 0) {
-          if (!warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
+      const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
+      if (grow) m = mt;
+      l *= f;
+      lt *= f;
+      const float ref = m == neg_inf() ? 0.f : m;
+      uint32_t pw[32];
+      if (whole)
+        la_row_weights<false>(va, vb, vis, sl2, ref, pw, l, lt);
+      else
+        la_row_weights<true>(va, vb, vis, sl2, ref, pw, l, lt);
+      if (i > 0) {
+        // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
+        if (!warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, grow)) {
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
             tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
@@ -637,43 +659,58 @@ __global__ void __launch_bounds__(kLaThreads, 1)
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
             tmem_st_32x32(trow + kLaColO + 32 * c, o);
           }
+          tmem_wait_st();
         }
       }
-      const float ref = m == neg_inf() ? 0.f : m;
-      uint32_t pw[32];
-      if (whole)
-        la_row_weights<false>(va, vb, vis, sl2, ref, pw, l, lt);
-      else
-        la_row_weights<true>(va, vb, vis, sl2, ref, pw, l, lt);
-      tmem_st_32x32(scol, pw);
-      tmem_wait_st();
+      // weights: row r of the K-major panel of 64 cache rows (128-byte swizzle), 8 rows a piece
+      uint8_t* prow = smem + kLaOffP + (hs == 64 ? half * kLaPanelBytes : 0) + r * 128;
+      if (hs == 64) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
+              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<uint4*>(prow + (((c + 2 * half) ^ (r & 7)) << 4)) =
+              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+      }
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->pfull[st]);
-      if (++vs == kLaVBufs) vs = 0;
+      if (lane == 0) la_arrive_at(pfull0);
     }
     // ------------------------------------------------------------ output
-    // The logits of the last tile say that the output of tile nt - 3 is complete, so its phase and the next
-    // one are waited for in turn (a wait for the last phase alone could meet the one two before it).
-    if (ok && nt > 1) ok = warp_wait(&bars->odone, (nt - 2) & 1, abort_flag);
     if (ok && nt > 0) ok = warp_wait(&bars->odone, (nt - 1) & 1, abort_flag);
-    if (ok) {
+    if (ok && nt > 0) {
+      // the row's sums: the two threads' halves
       tc_fence_after();
+      float* xl = xch;
+      xl[tl] = l;
+      xl[128 + tl] = lt;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->mx[grp]);
+      ok = warp_wait(&bars->mx[grp], nt & 1, abort_flag);
+      l += xl[tl ^ 64];
+      lt += xl[128 + (tl ^ 64)];
+    }
+    if (ok) {
       const bool empty = l == 0.f;                    // nothing visible (or only -inf logits)
       const float inv = empty ? 0.f : 1.f / lt;
-      const int64_t row = grow0 + r;
+      const int64_t row = grow0 + rq;
       const bool parts = P.n_split > 1;
-      if (vh == 0 && live) {
+      if (half == 0 && live) {
         const float v = empty ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
         if (parts)
           P.part_lse[static_cast<int64_t>(split) * P.T * H + row] = v;
         else if (P.lse)
           P.lse[row] = v;
       }
-      // rows through shared memory (free now: every copy and MMA of the CTA is done), so that a store covers
-      // a row's 512 bytes (one bulk copy per row took 3000 cycles to issue; this takes 600)
+      // rows through shared memory (the staged keys and values are read), so that a store covers 512 bytes of a
+      // row; chunk c of this lane is value columns 256 (c / 4) + 128 half + 32 (c % 4) ..
       const bool wide = parts || !P.out_bf16;
-      uint8_t* stage = smem + kLaOffV + r * (wide ? kLaOutPitch32 : kLaOutPitch16);
+      const int pitch = wide ? kLaOutPitch32 : kLaOutPitch16;
+      uint8_t* stage = smem + kLaOffK + r * pitch + 128 * half * (wide ? 4 : 2);
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
         if (nt > 0) {
@@ -682,12 +719,13 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+        const int col = 256 * (c >> 2) + 32 * (c & 3);
         if (wide) {
-          uint4* dst = reinterpret_cast<uint4*>(stage + 128 * c);
+          uint4* dst = reinterpret_cast<uint4*>(stage + 4 * col);
 #pragma unroll
           for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(stage + 64 * c);
+          uint4* dst = reinterpret_cast<uint4*>(stage + 2 * col);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t w[4];
@@ -702,20 +740,24 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       __syncwarp();
+      // each warp writes what it staged: 256 bytes (bf16: 128 columns) or 512 (fp32) at two places of a row, so
+      // half a warp takes one bf16 piece and a whole one an fp32 piece
       const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
       uint8_t* dst0 = parts ? reinterpret_cast<uint8_t*>(P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue)
                             : static_cast<uint8_t*>(P.out);
       const int size = wide ? 4 : 2;
-      const uint8_t* src0 = smem + kLaOffV + quad * 32 * (wide ? kLaOutPitch32 : kLaOutPitch16) + 16 * lane;
-      dst0 += ((grow0 + quad * 32) * kAttnValue + 256 * vh) * size + 16 * lane;
+      const int wrow = quad * 32 & 63;                // first row of the warp in this CTA
+      const int at = wide ? 512 * half + 16 * lane : 256 * half + 512 * (lane >> 4) + 16 * (lane & 15);
+      const uint8_t* src0 = smem + kLaOffK + wrow * pitch + at;
+      dst0 += (grow0 + kLaHalf * cr + wrow) * (kAttnValue * size) + at;
 #pragma unroll 8
-      for (int rr = 0; rr < 32; ++rr) {               // a warp writes its rows one by one, 512 bytes an access
+      for (int rr = 0; rr < 32; ++rr) {
         if (!((keep >> rr) & 1u)) continue;
         if (wide) {
           const uint4 v = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32);
-          const uint4 w = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32 + 512);
+          const uint4 w = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32 + 1024);
           *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4)) = v;
-          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4) + 512) = w;
+          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4) + 1024) = w;
         } else {
           *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 2)) =
               *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch16);
@@ -727,10 +769,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  la_cluster_sync();                                  // neither CTA ends while the other may read or signal it
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
 }
 
@@ -786,8 +829,8 @@ cudaError_t launch_latent_attn_combine(const LatentAttnParams& p, cudaStream_t s
 
 // Number of CTA pairs that share one tile of query rows.  `pairs` pairs cover
 // the query rows, each over at most `tiles` tiles of the cache; the machine
-// runs 74 pairs at once.  A tile costs about 1 us, a pair about 6 tiles more
-// for its query, its first copies and its output, and the combine about 4
+// runs 74 pairs at once.  A tile costs about 1.4 us, a pair about 5 tiles more
+// for its query, its first copies and its output, and the combine about 3
 // (with the launch): the split that makes the longest chain shortest.
 inline int la_splits(int64_t pairs, int64_t tiles) {
   int best = 1;
@@ -795,7 +838,7 @@ inline int la_splits(int64_t pairs, int64_t tiles) {
   const int64_t most = tiles < kLaMaxSplit ? tiles : kLaMaxSplit;
   for (int64_t s = 1; s <= (most > 1 ? most : 1); ++s) {
     const int64_t waves = (pairs * s + 73) / 74;
-    const int64_t cost = waves * ((tiles + s - 1) / s + 6) + (s > 1 ? 4 : 0);
+    const int64_t cost = waves * ((tiles + s - 1) / s + 5) + (s > 1 ? 3 : 0);
     if (s == 1 || cost < best_cost) {
       best = static_cast<int>(s);
       best_cost = cost;
