@@ -1716,7 +1716,7 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
   if (s != LS_OK) return s;
   {
     ProfScope prof("latent_attn_kernel", st);
-    LS_CUDA(launch_latent_attn(maps, p, st));
+    LS_CUDA(launch_latent_attn(maps, p, num_sms_current(), st));
   }
   if (p.n_split > 1) {
     ProfScope prof("latent_attn_combine_kernel", st);

@@ -78,7 +78,7 @@ constexpr int kLaMaxSplit = 64;
 
 struct LaBars {
   uint64_t qfull, k_full, v_full[2]; // first CTA: both CTAs' query rows, keys of a tile, value groups have landed
-  uint64_t k_empty[3], v_empty[2];   // key groups, value groups are read
+  uint64_t q_empty, k_empty[3], v_empty[2];   // query rows, key groups, value groups are read
   uint64_t v_seen;                   // a tile's values have landed in both CTAs (told by the first one's MMA warp)
   uint64_t sfull[2];                 // logits in tensor memory
   uint64_t pfull;                    // first CTA: both CTAs' weights in shared memory (8 warps)
@@ -96,10 +96,6 @@ constexpr size_t kLaOffBars = kLaOffX + 2 * 128 * sizeof(float);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
-// the output's rows on their way out, a 16-byte pad apart (lanes on different banks)
-constexpr int kLaOutPitch16 = kAttnValue * 2 + 16, kLaOutPitch32 = kAttnValue * 4 + 16;
-static_assert(kLaHalf * kLaOutPitch32 <= kLaOffP - kLaOffK, "output rows fit the staged keys and values");
-
 struct LatentAttnParams {
   const uint16_t* q = nullptr;        // [T * H][576]
   const int32_t* q_start = nullptr;   // [B + 1]
@@ -288,6 +284,20 @@ __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const u
   lt += la_sum2(c[0]);
 }
 
+// 128 bytes of each of a warp's 32 rows, staged with the 16-byte pieces of row i at their place ^ (i & 7), to rows
+// `pitch` bytes apart: eight lanes a row, four rows a store.
+__device__ __forceinline__ void la_rows_out(const uint8_t* stage, uint8_t* dst, int pitch, uint32_t keep, int lane) {
+  __syncwarp();
+  const int piece = lane & 7;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int i = 4 * u + (lane >> 3);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + i * 128 + ((piece ^ (i & 7)) << 4));
+    if ((keep >> i) & 1u) *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(i) * pitch + 16 * piece) = v;
+  }
+  __syncwarp();
+}
+
 // Tensor maps over rows of 9 panels of 64 elements, boxes of 64 elements x rows x panels, 128-byte swizzle.
 struct LaMaps {
   CUtensorMap q;            // q rows: 64 x 3 panels
@@ -295,52 +305,53 @@ struct LaMaps {
   CUtensorMap k_few, v_few; // latent rows: 16 x 3, 32 x 2
 };
 
-// grid: B * max_tiles * n_split pairs of CTAs.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
-    latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
-  extern __shared__ uint8_t la_raw[];
-  uint8_t* smem = smem_align1024(la_raw);
-  LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
-  volatile int* abort_flag = &bars->abort_flag;
-  // (broadcasts of what is the same in a warp anyway let the compiler keep it, and the MMAs' operands, uniform: an
-  // MMA whose operands move from a lane's registers takes 48 cycles to issue)
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-  const int lane = threadIdx.x & 31;
+// One unit of work: a tile of 128 query rows of a sequence over a part of the tiles that they see.
+struct LaItem {
+  int split, t0, n;        // part; the sequence's first token and number of tokens
+  int64_t r0, grow0;       // first query row in the sequence, in q
+  int nrows;               // query rows (at most 128)
+  int kv, avail;           // rows of the sequence, those that the cache holds (with the drafted ones)
+  int64_t off;             // its first row in the cache
+  LaSpan sp;
+  int i0, nt;              // tiles i0 .. i0 + nt - 1
+};
 
-  // ------------------------------------------------------------ this pair's work (the same in both CTAs)
-  int64_t bid = blockIdx.x;
-  const int cr = static_cast<int>(bid & 1);           // rank in the pair
-  bid >>= 1;
-  const int split = static_cast<int>(bid % P.n_split);
-  bid /= P.n_split;
-  const int qtile = static_cast<int>(bid % P.max_tiles);
-  const int b = static_cast<int>(bid / P.max_tiles);
+// Item `id`, the same in every warp of the pair; false where the grid covers no query rows.  Tables that do not hold
+// set the fault word (`tell`: the calling thread does that) and what they name wrongly is not seen.
+__device__ __forceinline__ bool la_item(const LatentAttnParams& P, int64_t id, bool tell, LaItem& w) {
+  w.split = static_cast<int>(id % P.n_split);
+  id /= P.n_split;
+  const int qtile = static_cast<int>(id % P.max_tiles);
+  const int b = static_cast<int>(id / P.max_tiles);
   const int H = P.H;
-  const int t0 = __ldg(P.q_start + b), t1 = __ldg(P.q_start + b + 1);
-  if (t0 < 0 || t1 < t0 || t1 > P.T) {                // not a prefix of the tokens: nothing of it is computed
-    if (threadIdx.x == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
-    return;
-  }
-  const int n = t1 - t0;
-  const int64_t seq_rows = static_cast<int64_t>(n) * H;
-  if (seq_rows > static_cast<int64_t>(P.max_tiles) * kLaRows && threadIdx.x == 0)
-    atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: the rest is not computed
-  const int64_t r0 = static_cast<int64_t>(qtile) * kLaRows;
-  if (r0 >= seq_rows) return;
-  const int nrows = static_cast<int>(seq_rows - r0 < kLaRows ? seq_rows - r0 : kLaRows);
-  const int64_t grow0 = static_cast<int64_t>(t0) * H + r0;          // first row in q / out
-  const int tok_first = static_cast<int>(r0 / H), tok_last = static_cast<int>((r0 + nrows - 1) / H);
-  const bool is_tree = P.tree != nullptr;
+  w.t0 = __ldg(P.q_start + b);
+  const int t1 = __ldg(P.q_start + b + 1);
   int kv = __ldg(P.kv_len + b);
   const int64_t off = P.row_off ? __ldg(P.row_off + b) : 0;
+  if (w.t0 < 0 || t1 < w.t0 || t1 > P.T) {            // not a prefix of the tokens: nothing of it is computed
+    if (tell) atomicOr(&g_fault, FAULT_BAD_INDEX);
+    return false;
+  }
+  const int n = w.n = t1 - w.t0;
+  const int64_t seq_rows = static_cast<int64_t>(n) * H;
+  if (seq_rows > static_cast<int64_t>(P.max_tiles) * kLaRows && tell)
+    atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: the rest is not computed
+  w.r0 = static_cast<int64_t>(qtile) * kLaRows;
+  if (w.r0 >= seq_rows) return false;
+  w.nrows = static_cast<int>(seq_rows - w.r0 < kLaRows ? seq_rows - w.r0 : kLaRows);
+  w.grow0 = static_cast<int64_t>(w.t0) * H + w.r0;
+  const int tok_first = static_cast<int>(w.r0 / H), tok_last = static_cast<int>((w.r0 + w.nrows - 1) / H);
+  const bool is_tree = P.tree != nullptr;
   const int own = is_tree ? n : 0;                    // drafted rows behind kv
-  if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && threadIdx.x == 0)
+  if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && tell)
     atomicOr(&g_fault, FAULT_BAD_INDEX);              // rows outside the cache are not seen
-  kv = kv < 0 ? 0 : kv > P.n_rows ? static_cast<int>(P.n_rows) : kv;
-  int avail = 0;                                      // rows of the sequence that the cache holds
+  w.kv = kv = kv < 0 ? 0 : kv > P.n_rows ? static_cast<int>(P.n_rows) : kv;
+  w.off = off;
+  int avail = 0;
   if (off >= 0 && off < P.n_rows)
     avail = static_cast<int>(P.n_rows - off < kv + static_cast<int64_t>(own) ? P.n_rows - off : kv + own);
-  LaSpan sp;
+  w.avail = avail;
+  LaSpan& sp = w.sp;
   if (is_tree) {
     const int ctx = kv < avail ? kv : avail;
     sp.drafted = avail - ctx;
@@ -366,12 +377,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   sp.n2 = (sp.drafted + kLaTile - 1) / kLaTile;
   const int all = sp.tiles();
   const int per = (all + P.n_split - 1) / P.n_split;
-  const int i0 = split * per < all ? split * per : all;
-  const int i1 = i0 + per < all ? i0 + per : all;
-  const int nt = __shfl_sync(0xffffffffu, i1 - i0, 0);
+  w.i0 = w.split * per < all ? w.split * per : all;
+  w.nt = (w.i0 + per < all ? w.i0 + per : all) - w.i0;
+  return true;
+}
+
+// Persistent: pair p of the grid takes the items p, p + pairs, ... of B * max_tiles * n_split.  The roles run through
+// the same items at their own pace: the next item's query, first tiles and logits are on their way while the
+// output of the last one leaves.  Barrier phases follow counts that run on over the items: tiles (g), items with
+// tiles (qn), exchanges (xn).
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
+    latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
+  extern __shared__ uint8_t la_raw[];
+  uint8_t* smem = smem_align1024(la_raw);
+  LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
+  volatile int* abort_flag = &bars->abort_flag;
+  // (broadcasts of what is the same in a warp anyway let the compiler keep it, and the MMAs' operands, uniform: an
+  // MMA whose operands move from a lane's registers takes 48 cycles to issue)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
+  const int cr = static_cast<int>(blockIdx.x & 1);    // rank in the pair
+  const int64_t items = static_cast<int64_t>(P.B) * P.max_tiles * P.n_split;
+  const int64_t item0 = blockIdx.x >> 1, item_step = gridDim.x >> 1;
+  const int H = P.H;
+  const bool is_tree = P.tree != nullptr;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->qfull, 1);
+    mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->k_full, kLaKGroups);
     for (int g = 0; g < kLaKGroups; ++g) mbar_init(&bars->k_empty[g], 1);
     mbar_init(&bars->v_seen, 1);
@@ -407,42 +440,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).
-    if (lane == 0 && nt > 0) {
+    if (lane == 0) {
       const bool first = cr == 0;
       const uint32_t qfull = la_map(&bars->qfull, 0), k_full = la_map(&bars->k_full, 0);
-      if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
-      for (int g = 0; g < kLaKGroups; ++g)
-        la_load_3d(smem + g * kLaKPer * kLaPanelBytes, &M.q, qfull, static_cast<int>(grow0 + kLaHalf * cr),
-                   kLaKPer * g);
+      const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
       bool ok = true;
-      // keys of tile i, then values of tile i - 1: the order in which their places become free
-      for (int i = 0; i <= nt && ok; ++i) {
-        if (i < nt) {
-          int kind, a, cnt;
-          sp.tile(i0 + i, kind, a, cnt);
-          const int box = la_box_rows(cnt) / 2;       // this CTA's half of the rows
-          const int row = static_cast<int>(off + a + (kind ? kv : 0)) + box * cr;
-          for (int g = 0; g < kLaKGroups; ++g) {
-            if (!mbar_wait(&bars->k_empty[g], (i & 1) ^ 1, abort_flag)) { ok = false; break; }
-            if (first) mbar_arrive_expect_tx(&bars->k_full, 2 * kLaKPer * box * 128);
-            la_load_3d(smem + kLaOffK + g * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full, row,
-                       kLaKPer * g);
+      int g = 0, qn = 0;
+      for (int64_t id = item0; id < items && ok; id += item_step) {
+        LaItem w;
+        if (!la_item(P, id, first, w) || w.nt == 0) continue;
+        if (!mbar_wait<false>(&bars->q_empty, (qn & 1) ^ 1, abort_flag)) { ok = false; break; }
+        ++qn;
+        if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
+        for (int c = 0; c < kLaKGroups; ++c)
+          la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, static_cast<int>(w.grow0 + kLaHalf * cr),
+                     kLaKPer * c);
+        // keys of tile i, then values of tile i - 1: the order in which their places become free
+        for (int i = 0; i <= w.nt && ok; ++i) {
+          if (i < w.nt) {
+            int kind, a, cnt;
+            w.sp.tile(w.i0 + i, kind, a, cnt);
+            const int box = la_box_rows(cnt) / 2;     // this CTA's half of the rows
+            const int row = static_cast<int>(w.off + a + (kind ? w.kv : 0)) + box * cr;
+            for (int c = 0; c < kLaKGroups; ++c) {
+              if (!mbar_wait<false>(&bars->k_empty[c], ((g + i) & 1) ^ 1, abort_flag)) { ok = false; break; }
+              if (first) mbar_arrive_expect_tx(&bars->k_full, 2 * kLaKPer * box * 128);
+              la_load_3d(smem + kLaOffK + c * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full, row,
+                         kLaKPer * c);
+            }
+          }
+          if (i > 0 && ok) {
+            const int j = i - 1;
+            int kind, a, cnt;
+            w.sp.tile(w.i0 + j, kind, a, cnt);
+            const int box = la_box_rows(cnt);
+            const int row = static_cast<int>(w.off + a + (kind ? w.kv : 0));
+            for (int c = 0; c < 2; ++c) {
+              // output MMA c has value columns 256 c .. : this CTA's 128 are panels 4 c + 2 cr and the next
+              if (!mbar_wait<false>(&bars->v_empty[c], ((g + j) & 1) ^ 1, abort_flag)) { ok = false; break; }
+              if (first) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
+              la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
+                         4 * c + 2 * cr);
+            }
           }
         }
-        if (i > 0 && ok) {
-          const int j = i - 1;
-          int kind, a, cnt;
-          sp.tile(i0 + j, kind, a, cnt);
-          const int box = la_box_rows(cnt);
-          const int row = static_cast<int>(off + a + (kind ? kv : 0));
-          for (int g = 0; g < 2; ++g) {
-            // output MMA g has value columns 256 g .. : this CTA's 128 of them are panels 4 g + 2 cr and the next
-            if (!mbar_wait(&bars->v_empty[g], (j & 1) ^ 1, abort_flag)) { ok = false; break; }
-            if (first) mbar_arrive_expect_tx(&bars->v_full[g], 2 * 2 * box * 128);
-            la_load_3d(smem + kLaOffV + g * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, la_map(&bars->v_full[g], 0),
-                       row, 4 * g + 2 * cr);
-          }
-        }
+        g += w.nt;
       }
       if (!ok) {
         // after an abort: the copies in flight (microseconds) land before the CTA ends
@@ -454,22 +496,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     // ------------------------------------------------------------ MMA issuer of the pair (first CTA)
     const uint32_t base = smem_u32(smem);
     constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, 256) | (1u << 16);   // B MN-major
-    bool ok = nt > 0 && cr == 0;
-    if (ok) ok = la_wait_all(&bars->qfull, 0, abort_flag);
+    bool ok = cr == 0;
     const uint64_t qdesc = sw128_kmajor_desc(base), kdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffK)),
                    pdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffP)),
                    vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
                    vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
     const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
+    int g = 0, qn = 0;
+    for (int64_t id = item0; id < items && ok; id += item_step) {
+    LaItem w;
+    if (!la_item(P, id, false, w) || w.nt == 0) continue;
+    const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+    if (!la_wait_all(&bars->qfull, qn & 1, abort_flag)) { ok = false; break; }
+    ++qn;
     bool full_prev = false;
-    for (int i = 0; i <= nt && ok; ++i) {
+    for (int i = 0; i <= nt && ok; ++i, ++g) {
       bool full = false;
       if (i < nt) {
         int kind, a, cnt;
-        sp.tile(i0 + i, kind, a, cnt);
+        w.sp.tile(w.i0 + i, kind, a, cnt);
         full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
-        const uint32_t d = tmem + kLaColS + 64 * (i & 1);
-        if (!la_wait_all(&bars->k_full, i & 1, abort_flag)) { ok = false; break; }
+        const uint32_t d = tmem + kLaColS + 64 * (g & 1);
+        if (!la_wait_all(&bars->k_full, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         // the two sizes apart, so that every descriptor is a constant away from one of two
         if (full) {
@@ -493,11 +541,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
             if (p % kLaKPer == kLaKPer - 1) la_commit_both(&bars->k_empty[p / kLaKPer]);
           }
         }
-        la_commit_both(&bars->sfull[i & 1]);
+        la_commit_both(&bars->sfull[g & 1]);
+        if (i == nt - 1) la_commit_both(&bars->q_empty);
       }
       if (i > 0) {                                    // the output of the tile before
-        const int j = i - 1;
-        if (!la_wait_all(&bars->v_full[0], j & 1, abort_flag) || !la_wait_all(&bars->v_full[1], j & 1, abort_flag)) {
+        const uint32_t ph = (g - 1) & 1;
+        if (!la_wait_all(&bars->v_full[0], ph, abort_flag) || !la_wait_all(&bars->v_full[1], ph, abort_flag)) {
           ok = false;
           break;
         }
@@ -506,30 +555,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           la_arrive_at(seen1);
         }
         __syncwarp();
-        if (!la_wait_all(&bars->pfull, j & 1, abort_flag)) { ok = false; break; }
+        if (!la_wait_all(&bars->pfull, ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t acc0 = j ? 1u : 0u;
+        const uint32_t acc0 = i > 1 ? 1u : 0u;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t d = tmem + kLaColO + 128 * g;
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t d = tmem + kLaColO + 128 * c;
           if (full_prev) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vdesc + (g * kLaVGroup + 2048 * s) / 16,
+              la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vdesc + (c * kLaVGroup + 2048 * s) / 16,
                      idesc_o, s ? 1u : acc0);
           } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-              la_mma(d, pdesc + 32 * s / 16, vdesc_few + (g * kLaVGroup + 2048 * s) / 16, idesc_o, s ? 1u : acc0);
+              la_mma(d, pdesc + 32 * s / 16, vdesc_few + (c * kLaVGroup + 2048 * s) / 16, idesc_o, s ? 1u : acc0);
           }
-          la_commit_both(&bars->v_empty[g]);
+          la_commit_both(&bars->v_empty[c]);
         }
         la_commit_both(&bars->odone);
       }
       full_prev = full;
     }
+    --g;                                              // the loop's last turn has no tile of its own
+    }
     // all MMAs this warp started are complete once `drain` flips
-    if (nt > 0 && cr == 0) {
+    if (cr == 0 && qn > 0) {
       la_commit_both(&bars->drain, 1);
       if (lane == 0) mbar_wait_drain(&bars->drain, 0);
       __syncwarp();
@@ -542,36 +593,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     const int grp = quad & 1;                         // the two warps that share 32 rows
     const int rq = kLaHalf * cr + r;                  // row of the pair
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const bool live = rq < nrows;
-    const int tok = static_cast<int>((r0 + (live ? rq : nrows - 1)) / H);
     float* xch = reinterpret_cast<float*>(smem + kLaOffX);
     const uint32_t pfull0 = la_map(&bars->pfull, 0);
+    // logits in log2 units; below 0 the logits' signs are turned instead
+    const bool turn = P.scale < 0.f;
+    const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
     bool ok = true;
+    int g = 0, xn = 0;
+    for (int64_t id = item0; id < items && ok; id += item_step) {
+    LaItem w;
+    if (!la_item(P, id, false, w)) continue;
+    const LaSpan& sp = w.sp;
+    const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+    const bool live = rq < w.nrows;
+    const int tok = static_cast<int>((w.r0 + (live ? rq : w.nrows - 1)) / H);
     // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
     int hi, lo;
     const uint64_t* branch = nullptr;
     if (is_tree) {
-      branch = P.tree + static_cast<int64_t>(t0 + tok) * P.words;
+      branch = P.tree + static_cast<int64_t>(w.t0 + tok) * P.words;
       int depth = 0;
       if (P.window > 0) {
-        for (int w = 0; w < P.words; ++w) depth += __popcll(__ldg(branch + w) & la_low_mask(n - 64 * w));
+        for (int c = 0; c < P.words; ++c) depth += __popcll(__ldg(branch + c) & la_low_mask(w.n - 64 * c));
         depth = depth > 0 ? depth - 1 : 0;
       }
       hi = sp.hi;
-      lo = la_window_lo(kv + depth, P.window, P.align);
+      lo = la_window_lo(w.kv + depth, P.window, P.align);
     } else {
-      const int p = kv - n + tok;
-      hi = p + 1 < avail ? p + 1 : avail;
+      const int p = w.kv - w.n + tok;
+      hi = p + 1 < w.avail ? p + 1 : w.avail;
       lo = la_window_lo(p, P.window, P.align);
     }
-    // logits in log2 units; below 0 the logits' signs are turned instead
-    const bool turn = P.scale < 0.f;
-    const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
     float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
-    for (int i = 0; i < nt && ok; ++i) {
-      const int st = i & 1;
+    for (int i = 0; i < nt && ok; ++i, ++g) {
+      const int st = g & 1;
       int kind, a0, cnt0;
-      sp.tile(i0 + i, kind, a0, cnt0);
+      sp.tile(w.i0 + i, kind, a0, cnt0);
       const bool whole = kind == 0 && cnt0 == kLaTile && a0 + kLaTile <= sp.hi_min &&
                          (a0 + kLaTile <= P.n_sink || a0 >= sp.lo_max);
       // this thread's rows of the tile: `hs` from a on, cnt of them in the tile
@@ -585,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         else
           vis = cnt > 0 ? (__ldg(branch + (a >> 6)) >> (a & 63)) & la_low_mask(cnt) : 0ull;
       }
-      if (!warp_wait(&bars->sfull[st], (i >> 1) & 1, abort_flag)) { ok = false; break; }
+      if (!warp_wait<false>(&bars->sfull[st], (g >> 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
       uint32_t va[32], vb[32];
       const uint32_t scol = trow + kLaColS + 64 * st;
@@ -608,13 +665,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
         // arrival (two warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
-          if ((i > 0 && !warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) ||
-              !warp_wait(&bars->v_seen, i & 1, abort_flag)) {
+          if ((i > 0 && !warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) ||
+              !warp_wait<false>(&bars->v_seen, g & 1, abort_flag)) {
             ok = false;
             break;
           }
-          for (int g = 0; g < 2; ++g) {
-            uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + g * kLaVGroup);
+          for (int c = 0; c < 2; ++c) {
+            uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + c * kLaVGroup);
             for (int e = lane; e < 2 * 8 * 2 * hs; e += 32) {
               uint4 x = v4[e];
               uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
@@ -633,7 +690,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       xch[128 * st + tl] = mt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      if (!warp_wait(&bars->mx[grp], i & 1, abort_flag)) { ok = false; break; }
+      if (!warp_wait<false>(&bars->mx[grp], xn & 1, abort_flag)) { ok = false; break; }
+      ++xn;
       mt = fmaxf(mt, xch[128 * st + (tl ^ 64)]);
       const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
       const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
@@ -648,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         la_row_weights<true>(va, vb, vis, sl2, ref, pw, l, lt);
       if (i > 0) {
         // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
-        if (!warp_wait(&bars->odone, (i - 1) & 1, abort_flag)) { ok = false; break; }
+        if (!warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (__any_sync(0xffffffffu, grow)) {
           for (int c = 0; c < 8; ++c) {
@@ -681,89 +739,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       if (lane == 0) la_arrive_at(pfull0);
     }
     // ------------------------------------------------------------ output
-    if (ok && nt > 0) ok = warp_wait(&bars->odone, (nt - 1) & 1, abort_flag);
+    if (ok && nt > 0) ok = warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag);
     if (ok && nt > 0) {
-      // the row's sums: the two threads' halves
+      // the row's sums: the two threads' halves (a second exchange says that both have read them)
       tc_fence_after();
-      float* xl = xch;
-      xl[tl] = l;
-      xl[128 + tl] = lt;
+      xch[tl] = l;
+      xch[128 + tl] = lt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      ok = warp_wait(&bars->mx[grp], nt & 1, abort_flag);
-      l += xl[tl ^ 64];
-      lt += xl[128 + (tl ^ 64)];
+      ok = warp_wait<false>(&bars->mx[grp], xn & 1, abort_flag);
+      l += xch[tl ^ 64];
+      lt += xch[128 + (tl ^ 64)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->mx[grp]);
+      if (ok) ok = warp_wait<false>(&bars->mx[grp], (xn + 1) & 1, abort_flag);
+      xn += 2;
     }
     if (ok) {
       const bool empty = l == 0.f;                    // nothing visible (or only -inf logits)
       const float inv = empty ? 0.f : 1.f / lt;
-      const int64_t row = grow0 + rq;
+      const int64_t row = w.grow0 + rq;
       const bool parts = P.n_split > 1;
+      const int64_t part0 = static_cast<int64_t>(w.split) * P.T * H;
       if (half == 0 && live) {
         const float v = empty ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
         if (parts)
-          P.part_lse[static_cast<int64_t>(split) * P.T * H + row] = v;
+          P.part_lse[part0 + row] = v;
         else if (P.lse)
           P.lse[row] = v;
       }
-      // rows through shared memory (the staged keys and values are read), so that a store covers 512 bytes of a
-      // row; chunk c of this lane is value columns 256 (c / 4) + 128 half + 32 (c % 4) ..
+      // Rows leave through the warp's 4 KB of the weights' place (free until its next weights), 128 bytes of each of
+      // its 32 rows at a time, so that a store covers four rows' whole lines.  Columns 32 c .. of this lane are
+      // value columns 256 (c / 4) + 128 half + 32 (c % 4) ...
       const bool wide = parts || !P.out_bf16;
-      const int pitch = wide ? kLaOutPitch32 : kLaOutPitch16;
-      uint8_t* stage = smem + kLaOffK + r * pitch + 128 * half * (wide ? 4 : 2);
+      const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
+      const int64_t row0 = w.grow0 + kLaHalf * cr + (quad & 1) * 32;                 // first row of the warp
+      uint8_t* dst = parts ? reinterpret_cast<uint8_t*>(P.part_o + part0 * kAttnValue) : static_cast<uint8_t*>(P.out);
+      dst += row0 * (kAttnValue * (wide ? 4 : 2));
+      uint8_t* stage = smem + kLaOffP + quad * 4096;
+      uint8_t* mine = stage + lane * 128;
+      uint32_t o[2][32];
+      if (nt > 0) tmem_ld_32x32_nowait(trow + kLaColO, o[0]);
+#pragma unroll
       for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
+        uint32_t(&x)[32] = o[c & 1];
         if (nt > 0) {
-          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
-          tmem_wait_ld(o);
+          tmem_wait_ld(x);
+          if (c < 7) tmem_ld_32x32_nowait(trow + kLaColO + 32 * (c + 1), o[(c + 1) & 1]);
         }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
-        const int col = 256 * (c >> 2) + 32 * (c & 3);
-        if (wide) {
-          uint4* dst = reinterpret_cast<uint4*>(stage + 4 * col);
+        for (int k = 0; k < 32; ++k) x[k] = empty ? 0u : __float_as_uint(__uint_as_float(x[k]) * inv);
+        const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+        if (wide) {                                   // 32 columns are 128 bytes
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(stage + 2 * col);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
+                make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          la_rows_out(stage, dst + 4 * col, kAttnValue * 4, keep, lane);
+        } else {                                      // 64 columns are
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+            uint32_t p2[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int e = 0; e < 4; ++e) {
               const __nv_bfloat162 h =
-                  __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * x]), __uint_as_float(o[8 * k + 2 * x + 1]));
-              w[x] = *reinterpret_cast<const uint32_t*>(&h);
+                  __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]), __uint_as_float(x[8 * k + 2 * e + 1]));
+              p2[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(mine + (((k + 4 * (c & 1)) ^ (lane & 7)) << 4)) =
+                make_uint4(p2[0], p2[1], p2[2], p2[3]);
           }
+          if (c & 1) la_rows_out(stage, dst + 2 * (col - 32), kAttnValue * 2, keep, lane);
         }
       }
-      __syncwarp();
-      // each warp writes what it staged: 256 bytes (bf16: 128 columns) or 512 (fp32) at two places of a row, so
-      // half a warp takes one bf16 piece and a whole one an fp32 piece
-      const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
-      uint8_t* dst0 = parts ? reinterpret_cast<uint8_t*>(P.part_o + static_cast<int64_t>(split) * P.T * H * kAttnValue)
-                            : static_cast<uint8_t*>(P.out);
-      const int size = wide ? 4 : 2;
-      const int wrow = quad * 32 & 63;                // first row of the warp in this CTA
-      const int at = wide ? 512 * half + 16 * lane : 256 * half + 512 * (lane >> 4) + 16 * (lane & 15);
-      const uint8_t* src0 = smem + kLaOffK + wrow * pitch + at;
-      dst0 += (grow0 + kLaHalf * cr + wrow) * (kAttnValue * size) + at;
-#pragma unroll 8
-      for (int rr = 0; rr < 32; ++rr) {
-        if (!((keep >> rr) & 1u)) continue;
-        if (wide) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32);
-          const uint4 w = *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch32 + 1024);
-          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4)) = v;
-          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 4) + 1024) = w;
-        } else {
-          *reinterpret_cast<uint4*>(dst0 + rr * (kAttnValue * 2)) =
-              *reinterpret_cast<const uint4*>(src0 + rr * kLaOutPitch16);
-        }
-      }
-      __syncwarp();
+    }
     }
   }
 
@@ -813,12 +862,13 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, cudaStream_t st) {
+cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, int num_sms, cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = smem_limit_once(attr_done, reinterpret_cast<const void*>(&latent_attn_kernel), kLaSmem);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(p.B) * p.max_tiles * p.n_split * 2;
-  latent_attn_kernel<<<static_cast<unsigned>(blocks), kLaThreads, kLaSmem, st>>>(maps, p);
+  const int64_t items = static_cast<int64_t>(p.B) * p.max_tiles * p.n_split;
+  const int64_t pairs = items < num_sms / 2 ? items : num_sms / 2;
+  latent_attn_kernel<<<static_cast<unsigned>(2 * pairs), kLaThreads, kLaSmem, st>>>(maps, p);
   return cudaGetLastError();
 }
 
