@@ -30,10 +30,11 @@
 // and the tensor core of each reads both CTAs' halves.  72 KB of query rows
 // and 16 KB of weights fill the shared memory.
 //
-//  - the first CTA of the pair issues all MMAs; both CTAs' copies report to
-//    its barriers;
-//  - the logits of tile i + 1 are issued before the output of tile i, so the
-//    softmax of a tile runs beside the MMAs of its neighbours;
+//  - the first CTA of the pair issues all MMAs, the logits' from one warp and
+//    the output's from another (one warp for both spent 800 cycles a tile in
+//    its waits); both CTAs' copies report to its barriers;
+//  - two tiles' logits are in flight, so the softmax of a tile runs beside the
+//    MMAs of its neighbours;
 //  - a row's logits of a tile lie in two lanes, so two threads share a row
 //    and exchange its maximum; the weights go to shared memory as bf16;
 //  - the output is rescaled only when a row's maximum grew by more than 16
@@ -71,7 +72,7 @@ constexpr int kLaPanels = kAttnLatent / 64;           // 9 panels of 64 elements
 constexpr int kLaKGroups = 3, kLaKPer = 3;            // the key panels' groups
 constexpr int kLaPanelBytes = kLaHalf * 128;          // 8 KB: 64 elements of 64 rows
 constexpr int kLaVGroup = 2 * kLaTile * 128;          // 32 KB: two value panels of 128 rows
-constexpr int kLaThreads = 6 * 32;                    // copies, MMA (first CTA), 4 softmax / epilogue warps
+constexpr int kLaThreads = 7 * 32;                    // copies, logit MMAs, output MMAs, 4 softmax / epilogue warps
 constexpr int kLaColO = 0, kLaColS = 256;             // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
 constexpr int kLaMaxSplit = 64;
@@ -79,20 +80,22 @@ constexpr int kLaMaxSplit = 64;
 struct LaBars {
   uint64_t qfull, k_full, v_full[2]; // first CTA: both CTAs' query rows, keys of a tile, value groups have landed
   uint64_t q_empty, k_empty[3], v_empty[2];   // query rows, key groups, value groups are read
-  uint64_t v_seen;                   // a tile's values have landed in both CTAs (told by the first one's MMA warp)
+  uint64_t v_seen;                   // the values of a tile that is not whole have landed in both CTAs
   uint64_t sfull[2];                 // logits in tensor memory
+  uint64_t s_empty[2];               // first CTA: both CTAs have read them (8 warps)
   uint64_t pfull;                    // first CTA: both CTAs' weights in shared memory (8 warps)
   uint64_t odone;                    // output MMAs of a tile are complete
   uint64_t mx[2];                    // the two warps that share 32 rows have written their maxima
-  uint64_t drain;
+  uint64_t drain[2];                 // all MMAs of an issuing warp are complete
   uint32_t tmem_base;
   int abort_flag;
 };
 constexpr size_t kLaOffK = size_t(kLaPanels) * kLaPanelBytes;               // behind the query rows
 constexpr size_t kLaOffV = kLaOffK + size_t(kLaPanels) * kLaPanelBytes;
 constexpr size_t kLaOffP = kLaOffV + 2 * size_t(kLaVGroup);
-constexpr size_t kLaOffX = kLaOffP + 2 * size_t(kLaPanelBytes);             // exchanged maxima / sums: 2 x 128 floats
-constexpr size_t kLaOffBars = kLaOffX + 2 * 128 * sizeof(float);
+constexpr size_t kLaOffX = kLaOffP + 2 * size_t(kLaPanelBytes);             // exchanged maxima: 2 x 128 floats
+constexpr size_t kLaOffL = kLaOffX + 2 * 128 * sizeof(float);               // exchanged sums: 128 + 64 floats
+constexpr size_t kLaOffBars = kLaOffL + 192 * sizeof(float);
 constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
 static_assert(sizeof(LaBars) <= 256, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
@@ -135,6 +138,10 @@ struct LaSpan {
   int n0, n1, n2;        // tiles of each
   int lo_max, hi_min;    // rows [lo_max, hi_min) are in every query row's window
   __device__ __forceinline__ int tiles() const { return n0 + n1 + n2; }
+  // whether every query row sees all of the tile
+  __device__ __forceinline__ bool whole(int kind, int a, int cnt, int n_sink) const {
+    return kind == 0 && cnt == kLaTile && a + kLaTile <= hi_min && (a + kLaTile <= n_sink || a >= lo_max);
+  }
   // kind 0: rows a .. a + cnt of the sequence; 1: drafted rows a .. a + cnt
   __device__ __forceinline__ void tile(int i, int& kind, int& a, int& cnt) const {
     kind = 0;
@@ -318,11 +325,12 @@ struct LaItem {
 
 // Item `id`, the same in every warp of the pair; false where the grid covers no query rows.  Tables that do not hold
 // set the fault word (`tell`: the calling thread does that) and what they name wrongly is not seen.
-__device__ __forceinline__ bool la_item(const LatentAttnParams& P, int64_t id, bool tell, LaItem& w) {
-  w.split = static_cast<int>(id % P.n_split);
-  id /= P.n_split;
-  const int qtile = static_cast<int>(id % P.max_tiles);
-  const int b = static_cast<int>(id / P.max_tiles);
+__device__ __forceinline__ bool la_item(const LatentAttnParams& P, uint32_t id, bool tell, LaItem& w) {
+  const uint32_t n_split = P.n_split, max_tiles = P.max_tiles;   // (32-bit divisions: the host checks the counts)
+  const uint32_t tile_id = id / n_split;
+  w.split = static_cast<int>(id - tile_id * n_split);
+  const int b = static_cast<int>(tile_id / max_tiles);
+  const int qtile = static_cast<int>(tile_id - b * max_tiles);
   const int H = P.H;
   w.t0 = __ldg(P.q_start + b);
   const int t1 = __ldg(P.q_start + b + 1);
@@ -340,7 +348,8 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int64_t id, b
   if (w.r0 >= seq_rows) return false;
   w.nrows = static_cast<int>(seq_rows - w.r0 < kLaRows ? seq_rows - w.r0 : kLaRows);
   w.grow0 = static_cast<int64_t>(w.t0) * H + w.r0;
-  const int tok_first = static_cast<int>(w.r0 / H), tok_last = static_cast<int>((w.r0 + w.nrows - 1) / H);
+  const uint32_t first_row = static_cast<uint32_t>(w.r0);        // T * H < 2^31
+  const int tok_first = first_row / static_cast<uint32_t>(H), tok_last = (first_row + w.nrows - 1) / static_cast<uint32_t>(H);
   const bool is_tree = P.tree != nullptr;
   const int own = is_tree ? n : 0;                    // drafted rows behind kv
   if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && tell)
@@ -397,8 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int cr = static_cast<int>(blockIdx.x & 1);    // rank in the pair
-  const int64_t items = static_cast<int64_t>(P.B) * P.max_tiles * P.n_split;
-  const int64_t item0 = blockIdx.x >> 1, item_step = gridDim.x >> 1;
+  const uint32_t items = static_cast<uint32_t>(P.B) * P.max_tiles * P.n_split;   // below 2^30
+  const uint32_t item0 = blockIdx.x >> 1, item_step = gridDim.x >> 1;
   const int H = P.H;
   const bool is_tree = P.tree != nullptr;
 
@@ -412,11 +421,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       mbar_init(&bars->v_full[g], 1);
       mbar_init(&bars->v_empty[g], 1);
       mbar_init(&bars->sfull[g], 1);
+      mbar_init(&bars->s_empty[g], 8);
       mbar_init(&bars->mx[g], 2);
     }
     mbar_init(&bars->pfull, 8);
     mbar_init(&bars->odone, 1);
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain[0], 1);
+    mbar_init(&bars->drain[1], 1);
     bars->abort_flag = 0;
     fence_barrier_init();
   }
@@ -446,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
       bool ok = true;
       int g = 0, qn = 0;
-      for (int64_t id = item0; id < items && ok; id += item_step) {
+      for (uint32_t id = item0; id < items && ok; id += item_step) {
         LaItem w;
         if (!la_item(P, id, first, w) || w.nt == 0) continue;
         if (!mbar_wait<false>(&bars->q_empty, (qn & 1) ^ 1, abort_flag)) { ok = false; break; }
@@ -493,31 +504,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer of the pair (first CTA)
+    // ------------------------------------------------------------ logit MMAs of the pair (first CTA)
     const uint32_t base = smem_u32(smem);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, 256) | (1u << 16);   // B MN-major
+    const uint64_t qdesc = sw128_kmajor_desc(base), kdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffK));
     bool ok = cr == 0;
-    const uint64_t qdesc = sw128_kmajor_desc(base), kdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffK)),
-                   pdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffP)),
-                   vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
-                   vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
-    const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
     int g = 0, qn = 0;
-    for (int64_t id = item0; id < items && ok; id += item_step) {
-    LaItem w;
-    if (!la_item(P, id, false, w) || w.nt == 0) continue;
-    const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
-    if (!la_wait_all(&bars->qfull, qn & 1, abort_flag)) { ok = false; break; }
-    ++qn;
-    bool full_prev = false;
-    for (int i = 0; i <= nt && ok; ++i, ++g) {
-      bool full = false;
-      if (i < nt) {
+    for (uint32_t id = item0; id < items && ok; id += item_step) {
+      LaItem w;
+      if (!la_item(P, id, false, w) || w.nt == 0) continue;
+      const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+      if (!la_wait_all(&bars->qfull, qn & 1, abort_flag)) { ok = false; break; }
+      ++qn;
+      for (int i = 0; i < nt; ++i, ++g) {
         int kind, a, cnt;
         w.sp.tile(w.i0 + i, kind, a, cnt);
-        full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
+        const bool full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
         const uint32_t d = tmem + kLaColS + 64 * (g & 1);
-        if (!la_wait_all(&bars->k_full, g & 1, abort_flag)) { ok = false; break; }
+        if (!la_wait_all(&bars->s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort_flag) ||
+            !la_wait_all(&bars->k_full, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         // the two sizes apart, so that every descriptor is a constant away from one of two
         if (full) {
@@ -531,37 +535,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           }
         } else {
           // few rows: a group's panels lie 16 rows apart
+#pragma unroll 1
+          for (int c = 0; c < kLaKGroups; ++c) {
+#pragma unroll 1
+            for (int p = 0; p < kLaKPer; ++p)
 #pragma unroll
-          for (int p = 0; p < kLaPanels; ++p) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              la_mma(d, qdesc + (p * kLaPanelBytes + 32 * kk) / 16,
-                     kdesc + (p / kLaKPer * kLaKPer * kLaPanelBytes + p % kLaKPer * (kLaFew * 64) + 32 * kk) / 16,
-                     idesc_bf16_f32(kLaRows, kLaFew), (p | kk) ? 1u : 0u);
-            if (p % kLaKPer == kLaKPer - 1) la_commit_both(&bars->k_empty[p / kLaKPer]);
+              for (int kk = 0; kk < 4; ++kk)
+                la_mma(d, qdesc + ((c * kLaKPer + p) * kLaPanelBytes + 32 * kk) / 16,
+                       kdesc + (c * kLaKPer * kLaPanelBytes + p * (kLaFew * 64) + 32 * kk) / 16,
+                       idesc_bf16_f32(kLaRows, kLaFew), (c | p | kk) ? 1u : 0u);
+            la_commit_both(&bars->k_empty[c]);
           }
         }
         la_commit_both(&bars->sfull[g & 1]);
         if (i == nt - 1) la_commit_both(&bars->q_empty);
       }
-      if (i > 0) {                                    // the output of the tile before
-        const uint32_t ph = (g - 1) & 1;
-        if (!la_wait_all(&bars->v_full[0], ph, abort_flag) || !la_wait_all(&bars->v_full[1], ph, abort_flag)) {
-          ok = false;
-          break;
+    }
+    // all MMAs this warp started are complete once `drain` flips
+    if (cr == 0 && qn > 0) {
+      la_commit_both(&bars->drain[0], 1);
+      if (lane == 0) mbar_wait_drain(&bars->drain[0], 0);
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ output MMAs of the pair (first CTA)
+    const uint32_t base = smem_u32(smem);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kLaRows, 256) | (1u << 16);   // B MN-major
+    const uint64_t pdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffP)),
+                   vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
+                   vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
+    const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
+    bool ok = cr == 0;
+    int g = 0;
+    for (uint32_t id = item0; id < items && ok; id += item_step) {
+      LaItem w;
+      if (!la_item(P, id, false, w)) continue;
+      const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+      for (int i = 0; i < nt; ++i, ++g) {
+        int kind, a, cnt;
+        w.sp.tile(w.i0 + i, kind, a, cnt);
+        const bool full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
+        if (!la_wait_all(&bars->v_full[0], g & 1, abort_flag)) { ok = false; break; }
+        if (!w.sp.whole(kind, a, cnt, P.n_sink)) {
+          if (!la_wait_all(&bars->v_full[1], g & 1, abort_flag)) { ok = false; break; }
+          if (lane == 0) {
+            la_arrive_at(seen0);
+            la_arrive_at(seen1);
+          }
+          __syncwarp();
         }
-        if (lane == 0) {
-          la_arrive_at(seen0);
-          la_arrive_at(seen1);
-        }
-        __syncwarp();
-        if (!la_wait_all(&bars->pfull, ph, abort_flag)) { ok = false; break; }
+        if (!la_wait_all(&bars->pfull, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t acc0 = i > 1 ? 1u : 0u;
+        const uint32_t acc0 = i ? 1u : 0u;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          if (c == 1) {
+            if (!la_wait_all(&bars->v_full[1], g & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+          }
           const uint32_t d = tmem + kLaColO + 128 * c;
-          if (full_prev) {
+          if (full) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
               la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vdesc + (c * kLaVGroup + 2048 * s) / 16,
@@ -573,21 +606,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           }
           la_commit_both(&bars->v_empty[c]);
         }
+        if (!ok) break;
         la_commit_both(&bars->odone);
       }
-      full_prev = full;
     }
-    --g;                                              // the loop's last turn has no tile of its own
-    }
-    // all MMAs this warp started are complete once `drain` flips
-    if (cr == 0 && qn > 0) {
-      la_commit_both(&bars->drain, 1);
-      if (lane == 0) mbar_wait_drain(&bars->drain, 0);
+    if (cr == 0 && g > 0) {
+      la_commit_both(&bars->drain[1], 1);
+      if (lane == 0) mbar_wait_drain(&bars->drain[1], 0);
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const int quad = warp & 3;                        // warps 2-5: tensor-memory lanes 32 * (warp & 3) ..
+    const int quad = warp & 3;                        // warps 3-6: tensor-memory lanes 32 * (warp & 3) ..
     const int tl = quad * 32 + lane;                  // tensor-memory lane
     const int r = tl & 63, half = tl >> 6;            // row of this CTA, and which half of a tile's rows
     const int grp = quad & 1;                         // the two warps that share 32 rows
@@ -599,14 +629,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     const bool turn = P.scale < 0.f;
     const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
     bool ok = true;
-    int g = 0, xn = 0;
-    for (int64_t id = item0; id < items && ok; id += item_step) {
+    const uint32_t s_read[2] = {la_map(&bars->s_empty[0], 0), la_map(&bars->s_empty[1], 0)};
+    float* xsum = reinterpret_cast<float*>(smem + kLaOffL);
+    int g = 0, xn = 0, vn = 0;                        // tiles, exchanges, tiles that are not whole
+    for (uint32_t id = item0; id < items && ok; id += item_step) {
     LaItem w;
     if (!la_item(P, id, false, w)) continue;
     const LaSpan& sp = w.sp;
     const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
     const bool live = rq < w.nrows;
-    const int tok = static_cast<int>((w.r0 + (live ? rq : w.nrows - 1)) / H);
+    const int tok = (static_cast<uint32_t>(w.r0) + (live ? rq : w.nrows - 1)) / static_cast<uint32_t>(H);
     // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
     int hi, lo;
     const uint64_t* branch = nullptr;
@@ -629,8 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       const int st = g & 1;
       int kind, a0, cnt0;
       sp.tile(w.i0 + i, kind, a0, cnt0);
-      const bool whole = kind == 0 && cnt0 == kLaTile && a0 + kLaTile <= sp.hi_min &&
-                         (a0 + kLaTile <= P.n_sink || a0 >= sp.lo_max);
+      const bool whole = sp.whole(kind, a0, cnt0, P.n_sink);
       // this thread's rows of the tile: `hs` from a on, cnt of them in the tile
       const int hs = la_box_rows(cnt0) / 2;
       const int a = a0 + hs * half;
@@ -650,6 +681,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       tmem_ld_32x32_nowait(scol + 32, vb);
       tmem_wait_ld(va);
       tmem_wait_ld(vb);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) la_arrive_at(s_read[st]);
       if (turn) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -666,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         // arrival (two warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
           if ((i > 0 && !warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) ||
-              !warp_wait<false>(&bars->v_seen, g & 1, abort_flag)) {
+              !warp_wait<false>(&bars->v_seen, vn & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -685,6 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           }
         }
       }
+      if (!whole) ++vn;
       // the row's maximum: this thread's half and, from the other warp of the pair, the other half
       float mt = la_row_max(va, vb, sl2);
       xch[128 * st + tl] = mt;
@@ -741,22 +776,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     // ------------------------------------------------------------ output
     if (ok && nt > 0) ok = warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag);
     if (ok && nt > 0) {
-      // the row's sums: the two threads' halves (a second exchange says that both have read them)
+      // the row's sums: the two threads' halves
       tc_fence_after();
-      xch[tl] = l;
-      xch[128 + tl] = lt;
+      xsum[tl] = lt;
+      if (half) xsum[128 + r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mx[grp]);
       ok = warp_wait<false>(&bars->mx[grp], xn & 1, abort_flag);
-      l += xch[tl ^ 64];
-      lt += xch[128 + (tl ^ 64)];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      if (ok) ok = warp_wait<false>(&bars->mx[grp], (xn + 1) & 1, abort_flag);
-      xn += 2;
+      ++xn;
+      lt += xsum[tl ^ 64];
+      if (!half) l += xsum[128 + r];
     }
     if (ok) {
-      const bool empty = l == 0.f;                    // nothing visible (or only -inf logits)
+      // nothing visible (or only -inf logits): the sum of the rounded weights is 0 exactly when that of the weights is
+      const bool empty = lt == 0.f;
       const float inv = empty ? 0.f : 1.f / lt;
       const int64_t row = w.grow0 + rq;
       const bool parts = P.n_split > 1;
@@ -778,39 +811,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       dst += row0 * (kAttnValue * (wide ? 4 : 2));
       uint8_t* stage = smem + kLaOffP + quad * 4096;
       uint8_t* mine = stage + lane * 128;
-      uint32_t o[2][32];
-      if (nt > 0) tmem_ld_32x32_nowait(trow + kLaColO, o[0]);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t(&x)[32] = o[c & 1];
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t x[2][32];
         if (nt > 0) {
-          tmem_wait_ld(x);
-          if (c < 7) tmem_ld_32x32_nowait(trow + kLaColO + 32 * (c + 1), o[(c + 1) & 1]);
+          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x[0]);
+          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c + 32, x[1]);
+          tmem_wait_ld(x[0]);
+          tmem_wait_ld(x[1]);
         }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = empty ? 0u : __float_as_uint(__uint_as_float(x[k]) * inv);
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
-        if (wide) {                                   // 32 columns are 128 bytes
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
-                make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          la_rows_out(stage, dst + 4 * col, kAttnValue * 4, keep, lane);
-        } else {                                      // 64 columns are
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t p2[4];
+          for (int k = 0; k < 32; ++k) x[u][k] = empty ? 0u : __float_as_uint(__uint_as_float(x[u][k]) * inv);
+          if (wide) {                                 // 32 columns are 128 bytes
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 h =
-                  __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]), __uint_as_float(x[8 * k + 2 * e + 1]));
-              p2[e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(x[u][4 * k], x[u][4 * k + 1], x[u][4 * k + 2], x[u][4 * k + 3]);
+            la_rows_out(stage, dst + 4 * (col + 32 * u), kAttnValue * 4, keep, lane);
+          } else {                                    // 64 columns are
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p2[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(x[u][8 * k + 2 * e]),
+                                                               __uint_as_float(x[u][8 * k + 2 * e + 1]));
+                p2[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(mine + (((k + 4 * u) ^ (lane & 7)) << 4)) =
+                  make_uint4(p2[0], p2[1], p2[2], p2[3]);
             }
-            *reinterpret_cast<uint4*>(mine + (((k + 4 * (c & 1)) ^ (lane & 7)) << 4)) =
-                make_uint4(p2[0], p2[1], p2[2], p2[3]);
           }
-          if (c & 1) la_rows_out(stage, dst + 2 * (col - 32), kAttnValue * 2, keep, lane);
         }
+        if (!wide) la_rows_out(stage, dst + 2 * col, kAttnValue * 2, keep, lane);
       }
     }
     }
