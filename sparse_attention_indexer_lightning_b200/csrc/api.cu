@@ -1624,7 +1624,7 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
 
 namespace {
 
-// Tiles of the cache that one tile of query rows can meet, at most.
+// Tiles of the cache that one tile of query rows can meet, at most (as far as the host knows).
 int64_t span_tiles(int H, int max_q, int64_t ctx, int window, int align, int n_sink, int drafted) {
   int64_t span = ctx;                                 // the whole context
   int64_t sinks = 0;
@@ -1643,10 +1643,11 @@ int query_tiles(int H, int max_q) {
   return static_cast<int>((static_cast<int64_t>(max_q) * H + kLaRows - 1) / kLaRows);
 }
 
-size_t span_workspace(int T, int H, int n_split) {
-  if (n_split <= 1) return 0;
-  const size_t rows = static_cast<size_t>(n_split) * T * H;
-  return align_up(rows * kAttnValue * sizeof(float)) + align_up(rows * sizeof(float));
+size_t span_workspace(const LaLayout& l) {
+  if (!l.cut) return 0;
+  const size_t rows = 2 * static_cast<size_t>(l.pairs) * kLaRows;
+  return align_up(rows * kAttnValue * sizeof(float)) + align_up(rows * sizeof(float)) +
+         align_up(static_cast<size_t>(l.pairs) * sizeof(LaJoin));
 }
 
 bool span_sizes_ok(int B, int T, int H, int max_q, int window, int align, int n_sink, bool tree) {
@@ -1655,14 +1656,14 @@ bool span_sizes_ok(int B, int T, int H, int max_q, int window, int align, int n_
          static_cast<int64_t>(window) + align <= (1 << 30);
 }
 
-int window_splits(int B, int H, int max_q, int window, int align, int n_sink) {
-  return la_splits(static_cast<int64_t>(B) * query_tiles(H, max_q),
+LaLayout window_layout(int B, int H, int max_q, int window, int align, int n_sink) {
+  return la_layout(static_cast<int64_t>(B) * query_tiles(H, max_q),
                    span_tiles(H, max_q, 0, window, align, n_sink, 0));
 }
 
-int tree_splits(int B, int H, int max_q, int64_t n_rows, int max_ctx, int window, int align, int n_sink) {
+LaLayout tree_layout(int B, int H, int max_q, int64_t n_rows, int max_ctx, int window, int align, int n_sink) {
   const int64_t ctx = max_ctx > 0 && max_ctx < n_rows ? max_ctx : n_rows;
-  return la_splits(static_cast<int64_t>(B) * query_tiles(H, max_q),
+  return la_layout(static_cast<int64_t>(B) * query_tiles(H, max_q),
                    span_tiles(H, max_q, ctx, window, align, n_sink, max_q));
 }
 
@@ -1683,7 +1684,7 @@ ls_status make_panel_map(CUtensorMap* m, const void* base, uint64_t rows, uint32
 }
 
 // Shared checks, tensor maps and launches of the two span attentions.
-ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* latent, int max_q, int out_dtype,
+ls_status span_attention(LatentAttnParams p, const LaLayout& lay, int d, int d_v, const uint16_t* latent, int max_q, int out_dtype,
                          void* ws, size_t ws_bytes, cudaStream_t st) {
   if (d != kAttnLatent || d_v != kAttnValue)
     return fail(LS_ERR_UNSUPPORTED, "latent rows of %d elements with %d value elements are built (got d=%d d_v=%d)",
@@ -1696,15 +1697,19 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
   LS_CHECK_ARG(p.q && latent && p.q_start && p.kv_len && p.out, "null tensor pointer");
   LS_CHECK_ARG(aligned16(p.q) && aligned16(latent) && aligned16(p.out), "q, latent and out must be 16-byte aligned");
   p.max_tiles = query_tiles(p.H, max_q);
-  LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles * p.n_split * 2 <= 0x7fffffffLL, "B * max_q * H too large");
+  LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles <= (1 << 30), "B * max_q * H too large");
+  p.pairs = lay.pairs;
+  p.cut = lay.cut;
   p.out_bf16 = out_dtype == LS_OUT_BF16;
-  const size_t need = span_workspace(p.T, p.H, p.n_split);
+  const size_t need = span_workspace(lay);
   if (need > 0) {
     if (ws_bytes < need) return fail(LS_ERR_WORKSPACE, "workspace of %zu B, %zu B needed", ws_bytes, need);
     LS_CHECK_ARG(ws && aligned16(ws), "the workspace must be a 16-byte aligned device pointer");
     Carver c(ws);
-    p.part_o = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H * kAttnValue);
-    p.part_lse = c.take<float>(static_cast<size_t>(p.n_split) * p.T * p.H);
+    const size_t rows = 2 * static_cast<size_t>(p.pairs) * kLaRows;
+    p.part_o = c.take<float>(rows * kAttnValue);
+    p.part_lse = c.take<float>(rows);
+    p.joins = c.take<LaJoin>(p.pairs);
   }
   LaMaps maps;
   const uint64_t q_rows = static_cast<uint64_t>(p.T) * p.H, kv_rows = static_cast<uint64_t>(p.n_rows);
@@ -1716,9 +1721,9 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
   if (s != LS_OK) return s;
   {
     ProfScope prof("latent_attn_kernel", st);
-    LS_CUDA(launch_latent_attn(maps, p, num_sms_current(), st));
+    LS_CUDA(launch_latent_attn(maps, p, st));
   }
-  if (p.n_split > 1) {
+  if (p.cut) {
     ProfScope prof("latent_attn_combine_kernel", st);
     LS_CUDA(launch_latent_attn_combine(p, st));
   }
@@ -1729,7 +1734,7 @@ ls_status span_attention(LatentAttnParams p, int d, int d_v, const uint16_t* lat
 
 size_t ls_window_attention_workspace_size(int B, int T, int H, int max_q, int window, int align, int n_sink) {
   if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, false) || B == 0 || T == 0 || max_q == 0) return 0;
-  return span_workspace(T, H, window_splits(B, H, std::min(max_q, T), window, align, n_sink));
+  return span_workspace(window_layout(B, H, std::min(max_q, T), window, align, n_sink));
 }
 
 ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
@@ -1756,15 +1761,16 @@ ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const i
   p.scale = scale;
   p.out = out;
   p.lse = lse;
-  if (B > 0 && max_q > 0) p.n_split = window_splits(B, H, max_q, window, align, n_sink);
-  return span_attention(p, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
+  LaLayout lay{1, 0};
+  if (B > 0 && max_q > 0) lay = window_layout(B, H, max_q, window, align, n_sink);
+  return span_attention(p, lay, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
 }
 
 size_t ls_tree_attention_workspace_size(int B, int T, int H, int max_q, int64_t n_rows, int max_ctx, int window,
                                         int align, int n_sink) {
   if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, true) || n_rows < 1 || B == 0 || T == 0 || max_q == 0)
     return 0;
-  return span_workspace(T, H, tree_splits(B, H, std::min(max_q, T), n_rows, max_ctx, window, align, n_sink));
+  return span_workspace(tree_layout(B, H, std::min(max_q, T), n_rows, max_ctx, window, align, n_sink));
 }
 
 ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
@@ -1796,9 +1802,10 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
   p.scale = scale;
   p.out = out;
   p.lse = lse;
+  LaLayout lay{1, 0};
   if (B > 0 && max_q > 0 && n_rows >= 1)
-    p.n_split = tree_splits(B, H, max_q, n_rows, max_ctx, window, align, n_sink);
-  return span_attention(p, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
+    lay = tree_layout(B, H, max_q, n_rows, max_ctx, window, align, n_sink);
+  return span_attention(p, lay, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
 }
 
 ls_status ls_norm_rope(const ls_norm_rows* q, const ls_norm_rows* k, const int64_t* pos, const float* inv_freq,

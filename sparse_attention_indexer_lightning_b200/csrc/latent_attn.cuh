@@ -53,9 +53,12 @@
 // times one of them would be NaN) and cleared.  A visible row with a NaN or
 // +inf logit makes its own query row NaN, and no other.
 //
-// Few query rows over a long span: the tiles are split over n_split CTA pairs,
-// each writing its part (fp32, with its lse) to the workspace, and
-// latent_attn_combine_kernel joins the parts.
+// Query rows that would leave pairs idle (few of them over a long span, or
+// sequences of very different lengths): the tiles of all of them, laid out one
+// after another, are cut into equal runs, one per pair (LaIter).  An item that
+// a cut goes through is written in parts (fp32, with their lse) to the
+// workspace, at most two parts a pair, and latent_attn_combine_kernel joins
+// them.
 
 #pragma once
 
@@ -72,52 +75,10 @@ constexpr int kLaPanels = kAttnLatent / 64;           // 9 panels of 64 elements
 constexpr int kLaKGroups = 3, kLaKPer = 3;            // the key panels' groups
 constexpr int kLaPanelBytes = kLaHalf * 128;          // 8 KB: 64 elements of 64 rows
 constexpr int kLaVGroup = 2 * kLaTile * 128;          // 32 KB: two value panels of 128 rows
-constexpr int kLaThreads = 7 * 32;                    // copies, logit MMAs, output MMAs, 4 softmax / epilogue warps
+constexpr int kLaThreads = 8 * 32;   // query and key copies, logit MMAs, output MMAs, 4 softmax / epilogue, value copies
 constexpr int kLaColO = 0, kLaColS = 256;             // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
-constexpr int kLaMaxSplit = 64;
-
-struct LaBars {
-  uint64_t qfull, k_full, v_full[2]; // first CTA: both CTAs' query rows, keys of a tile, value groups have landed
-  uint64_t q_empty, k_empty[3], v_empty[2];   // query rows, key groups, value groups are read
-  uint64_t v_seen;                   // the values of a tile that is not whole have landed in both CTAs
-  uint64_t sfull[2];                 // logits in tensor memory
-  uint64_t s_empty[2];               // first CTA: both CTAs have read them (8 warps)
-  uint64_t pfull;                    // first CTA: both CTAs' weights in shared memory (8 warps)
-  uint64_t odone;                    // output MMAs of a tile are complete
-  uint64_t mx[2];                    // the two warps that share 32 rows have written their maxima
-  uint64_t drain[2];                 // all MMAs of an issuing warp are complete
-  uint32_t tmem_base;
-  int abort_flag;
-};
-constexpr size_t kLaOffK = size_t(kLaPanels) * kLaPanelBytes;               // behind the query rows
-constexpr size_t kLaOffV = kLaOffK + size_t(kLaPanels) * kLaPanelBytes;
-constexpr size_t kLaOffP = kLaOffV + 2 * size_t(kLaVGroup);
-constexpr size_t kLaOffX = kLaOffP + 2 * size_t(kLaPanelBytes);             // exchanged maxima: 2 x 128 floats
-constexpr size_t kLaOffL = kLaOffX + 2 * 128 * sizeof(float);               // exchanged sums: 128 + 64 floats
-constexpr size_t kLaOffBars = kLaOffL + 192 * sizeof(float);
-constexpr size_t kLaSmem = 1024 /*align slack*/ + kLaOffBars + 256;
-static_assert(sizeof(LaBars) <= 256, "barrier block");
-static_assert(kLaSmem <= 232448, "shared memory budget");
-struct LatentAttnParams {
-  const uint16_t* q = nullptr;        // [T * H][576]
-  const int32_t* q_start = nullptr;   // [B + 1]
-  const int32_t* kv_len = nullptr;    // [B]: window: rows with the tokens' own; tree: context rows
-  const int64_t* row_off = nullptr;   // [B] or nullptr (0)
-  const uint64_t* tree = nullptr;     // [T][words] or nullptr: the window form
-  int words = 0;
-  int B = 0, T = 0, H = 0;
-  int max_tiles = 0;                  // 128-row tiles per sequence that the grid covers
-  int64_t n_rows = 0;
-  int window = 0, align = 1, n_sink = 0;   // window <= 0 (tree only): the whole context
-  float scale = 0.f;
-  int n_split = 1;
-  int out_bf16 = 0;
-  void* out = nullptr;                // [T * H][512]
-  float* lse = nullptr;               // [T * H] or nullptr
-  float* part_o = nullptr;            // [n_split][T * H][512]
-  float* part_lse = nullptr;          // [n_split][T * H]
-};
+constexpr int kLaItemCost = 2;                        // an item's own cost in tiles: its query, its output
 
 // First row of the window of the token at position p.
 __host__ __device__ inline int la_window_lo(int p, int window, int align) {
@@ -160,6 +121,75 @@ struct LaSpan {
   }
 };
 
+// One unit of work: a tile of 128 query rows of a sequence over the tiles that they see, or a part of these.
+struct LaItem {
+  int part;                // its place among the parts, -1: whole
+  int t0, n;               // the sequence's first token and number of tokens
+  int r0, grow0;           // first query row in the sequence, in q (T * H < 2^31)
+  int nrows;               // query rows (at most 128)
+  int kv, avail;           // rows of the sequence, those that the cache holds (with the drafted ones)
+  int row0, rowd;          // cache rows of its row 0 and of its first drafted row (n_rows + T < 2^31)
+  LaSpan sp;
+  int i0, nt;              // tiles i0 .. i0 + nt - 1; nt < 0: there are no more items
+};
+constexpr int kLaItems = 3;   // items in shared memory: the copies' warp writes them, the other roles read them
+
+struct LaBars {
+  uint64_t qfull, k_full[3], v_full[2];   // first CTA: both CTAs' query rows, key groups, value groups have landed
+  uint64_t q_empty, k_empty[3], v_empty[2];   // query rows, key groups, value groups are read
+  uint64_t v_seen;                   // the values of a tile that is not whole have landed in both CTAs
+  uint64_t sfull[2];                 // logits in tensor memory
+  uint64_t s_empty[2];               // first CTA: both CTAs have read them (8 warps)
+  uint64_t pfull;                    // first CTA: both CTAs' weights in shared memory (8 warps)
+  uint64_t odone;                    // output MMAs of a tile are complete
+  uint64_t mx[2];                    // the two warps that share 32 rows have written their maxima
+  uint64_t item_full[kLaItems], item_empty[kLaItems];
+  uint64_t drain[2];                 // all MMAs of an issuing warp are complete
+  uint32_t tmem_base;
+  int abort_flag;
+  int64_t run_pos, run_end, run_base, run_total;      // cut form: this pair's run, see LaIter
+  int run_seq;
+  LaItem item[kLaItems];
+};
+constexpr size_t kLaOffK = size_t(kLaPanels) * kLaPanelBytes;               // behind the query rows
+constexpr size_t kLaOffV = kLaOffK + size_t(kLaPanels) * kLaPanelBytes;
+constexpr size_t kLaOffP = kLaOffV + 2 * size_t(kLaVGroup);
+constexpr size_t kLaOffX = kLaOffP + 2 * size_t(kLaPanelBytes);             // exchanged maxima: 2 x 128 floats
+constexpr size_t kLaOffL = kLaOffX + 2 * 128 * sizeof(float);               // exchanged sums: 128 + 64 floats
+constexpr size_t kLaOffBars = kLaOffL + 192 * sizeof(float);
+constexpr size_t kLaSmem = kLaOffBars + 640;
+static_assert(sizeof(LaBars) <= 640, "barrier block");
+static_assert(kLaSmem <= 232448, "shared memory budget");
+struct LatentAttnParams {
+  const uint16_t* q = nullptr;        // [T * H][576]
+  const int32_t* q_start = nullptr;   // [B + 1]
+  const int32_t* kv_len = nullptr;    // [B]: window: rows with the tokens' own; tree: context rows
+  const int64_t* row_off = nullptr;   // [B] or nullptr (0)
+  const uint64_t* tree = nullptr;     // [T][words] or nullptr: the window form
+  int words = 0;
+  int B = 0, T = 0, H = 0;
+  int max_tiles = 0;                  // 128-row tiles per sequence that the grid covers
+  int64_t n_rows = 0;
+  int window = 0, align = 1, n_sink = 0;   // window <= 0 (tree only): the whole context
+  float scale = 0.f;
+  int pairs = 1;                      // CTA pairs of the grid
+  int cut = 0;                        // equal runs of tiles per pair; else whole items in turn
+  int out_bf16 = 0;
+  void* out = nullptr;                // [T * H][512]
+  float* lse = nullptr;               // [T * H] or nullptr
+  // cut form: pair p's part of the item that its run begins inside of (2 p) and that it ends inside of (2 p + 1)
+  float* part_o = nullptr;            // [2 * pairs][128][512]
+  float* part_lse = nullptr;          // [2 * pairs][128]
+  struct LaJoin* joins = nullptr;     // [pairs]
+};
+
+// The item that pair p's run ends inside of, if it begins there too: its first row, its rows, and how many pairs have
+// a part of it (0: there is none).
+struct LaJoin {
+  int64_t row0;
+  int nrows, parts;
+};
+
 // Box of 64 elements x rows x panels (y the row, z the panel) into this CTA's shared memory, reported to a barrier
 // of the pair (a cluster address).
 __device__ __forceinline__ void la_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int y, int z) {
@@ -168,6 +198,12 @@ __device__ __forceinline__ void la_load_3d(void* dst, const CUtensorMap* map, ui
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y), "r"(z)
       : "memory");
+}
+
+// After an abort: the copies in flight (microseconds) land before the CTA ends.
+__device__ __forceinline__ void la_settle() {
+  const uint64_t t = globaltimer_ns();
+  while (globaltimer_ns() - t < 1000000ull) __nanosleep(1000);
 }
 
 // Rows of a tile as it is staged.
@@ -237,16 +273,16 @@ __device__ __forceinline__ void la_commit_both(uint64_t* bar, uint16_t mask = 3)
       : "memory");
 }
 
-// Sets the masked places of 32 logits to -inf; whether one of the places
-// `there` that the MMAs wrote was not finite.
-__device__ __forceinline__ bool la_mask_row(uint32_t (&v)[32], uint32_t vis, uint32_t there) {
-  bool bad = false;
+// Sets the masked places of 32 logits to -inf; whether one of the 32 (stale ones among them) was not finite.
+__device__ __forceinline__ bool la_mask_row(uint32_t (&v)[32], uint32_t vis) {
+  uint32_t top = 0u;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    if (there & (1u << j)) bad |= (v[j] & 0x7f800000u) == 0x7f800000u;
+    const uint32_t mag = v[j] & 0x7fffffffu;
+    top = top > mag ? top : mag;
     if (!(vis & (1u << j))) v[j] = 0xff800000u;
   }
-  return bad;
+  return top >= 0x7f800000u;
 }
 
 // One row's largest logit of a tile in log2 units (masked places hold -inf).
@@ -259,11 +295,9 @@ __device__ __forceinline__ float la_row_max(const uint32_t (&va)[32], const uint
 }
 
 // One row's weights of a tile, packed to bf16 pairs, and their sums: of the weights and of the rounded weights.
-// Masked places hold -inf and weigh 0 (a scale of 0 takes them out by the mask: 0 * -inf is NaN).
-template <bool MASKED>
-__device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const uint32_t (&vb)[32], uint64_t vis,
-                                               float sl2, float ref, uint32_t (&pw)[32], float& l, float& lt) {
-  const uint32_t vlo = static_cast<uint32_t>(vis), vhi = static_cast<uint32_t>(vis >> 32);
+// Masked places hold -inf and weigh 0 (sl2 is not 0).
+__device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const uint32_t (&vb)[32], float sl2,
+                                               float ref, uint32_t (&pw)[32], float& l, float& lt) {
   const uint64_t s2 = pack_f32x2(sl2, sl2), r2 = pack_f32x2(-ref, -ref);
   uint64_t a[2] = {0ull, 0ull}, c[2] = {0ull, 0ull};
 #pragma unroll
@@ -275,11 +309,6 @@ __device__ __forceinline__ void la_row_weights(const uint32_t (&va)[32], const u
     unpack_f32x2(z, p0, p1);
     p0 = la_exp2(p0);
     p1 = la_exp2(p1);
-    if (MASKED) {
-      const uint32_t w = e < 16 ? vlo : vhi;
-      if (!(w & (1u << ((2 * e) & 31)))) p0 = 0.f;
-      if (!(w & (1u << ((2 * e + 1) & 31)))) p1 = 0.f;
-    }
     la_add2(a[e & 1], pack_f32x2(p0, p1));
     const __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
     pw[e] = *reinterpret_cast<const uint32_t*>(&pb);
@@ -312,25 +341,10 @@ struct LaMaps {
   CUtensorMap k_few, v_few; // latent rows: 16 x 3, 32 x 2
 };
 
-// One unit of work: a tile of 128 query rows of a sequence over a part of the tiles that they see.
-struct LaItem {
-  int split, t0, n;        // part; the sequence's first token and number of tokens
-  int64_t r0, grow0;       // first query row in the sequence, in q
-  int nrows;               // query rows (at most 128)
-  int kv, avail;           // rows of the sequence, those that the cache holds (with the drafted ones)
-  int64_t off;             // its first row in the cache
-  LaSpan sp;
-  int i0, nt;              // tiles i0 .. i0 + nt - 1
-};
-
-// Item `id`, the same in every warp of the pair; false where the grid covers no query rows.  Tables that do not hold
-// set the fault word (`tell`: the calling thread does that) and what they name wrongly is not seen.
-__device__ __forceinline__ bool la_item(const LatentAttnParams& P, uint32_t id, bool tell, LaItem& w) {
-  const uint32_t n_split = P.n_split, max_tiles = P.max_tiles;   // (32-bit divisions: the host checks the counts)
-  const uint32_t tile_id = id / n_split;
-  w.split = static_cast<int>(id - tile_id * n_split);
-  const int b = static_cast<int>(tile_id / max_tiles);
-  const int qtile = static_cast<int>(tile_id - b * max_tiles);
+// Query tile `qtile` of sequence b (-1: its last), whole; false where the sequence has none.  `all` is the number of
+// query tiles.  Tables that do not hold set the fault word (`tell`: the calling thread does that) and what they name
+// wrongly is not seen.
+__device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qtile, bool tell, LaItem& w, int& all) {
   const int H = P.H;
   w.t0 = __ldg(P.q_start + b);
   const int t1 = __ldg(P.q_start + b + 1);
@@ -344,10 +358,13 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, uint32_t id, 
   const int64_t seq_rows = static_cast<int64_t>(n) * H;
   if (seq_rows > static_cast<int64_t>(P.max_tiles) * kLaRows && tell)
     atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: the rest is not computed
-  w.r0 = static_cast<int64_t>(qtile) * kLaRows;
-  if (w.r0 >= seq_rows) return false;
+  const int tiles = static_cast<int>((static_cast<uint32_t>(seq_rows) + kLaRows - 1) / kLaRows);   // T * H < 2^31
+  all = tiles < P.max_tiles ? tiles : P.max_tiles;
+  if (qtile < 0) qtile = all - 1;
+  if (qtile < 0 || qtile >= all) return false;
+  w.r0 = qtile * kLaRows;
   w.nrows = static_cast<int>(seq_rows - w.r0 < kLaRows ? seq_rows - w.r0 : kLaRows);
-  w.grow0 = static_cast<int64_t>(w.t0) * H + w.r0;
+  w.grow0 = w.t0 * H + w.r0;
   const uint32_t first_row = static_cast<uint32_t>(w.r0);        // T * H < 2^31
   const int tok_first = first_row / static_cast<uint32_t>(H), tok_last = (first_row + w.nrows - 1) / static_cast<uint32_t>(H);
   const bool is_tree = P.tree != nullptr;
@@ -355,11 +372,12 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, uint32_t id, 
   if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && tell)
     atomicOr(&g_fault, FAULT_BAD_INDEX);              // rows outside the cache are not seen
   w.kv = kv = kv < 0 ? 0 : kv > P.n_rows ? static_cast<int>(P.n_rows) : kv;
-  w.off = off;
   int avail = 0;
   if (off >= 0 && off < P.n_rows)
     avail = static_cast<int>(P.n_rows - off < kv + static_cast<int64_t>(own) ? P.n_rows - off : kv + own);
   w.avail = avail;
+  w.row0 = avail > 0 ? static_cast<int>(off) : 0;
+  w.rowd = w.row0 + kv;
   LaSpan& sp = w.sp;
   if (is_tree) {
     const int ctx = kv < avail ? kv : avail;
@@ -384,21 +402,154 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, uint32_t id, 
   sp.n0 = (sp.sink_len + kLaTile - 1) / kLaTile;
   sp.n1 = sp.hi > sp.lo ? (sp.hi - sp.lo + kLaTile - 1) / kLaTile : 0;
   sp.n2 = (sp.drafted + kLaTile - 1) / kLaTile;
-  const int all = sp.tiles();
-  const int per = (all + P.n_split - 1) / P.n_split;
-  w.i0 = w.split * per < all ? w.split * per : all;
-  w.nt = (w.i0 + per < all ? w.i0 + per : all) - w.i0;
+  w.part = -1;
+  w.i0 = 0;
+  w.nt = sp.tiles();
   return true;
 }
 
-// Persistent: pair p of the grid takes the items p, p + pairs, ... of B * max_tiles * n_split.  The roles run through
-// the same items at their own pace: the next item's query, first tiles and logits are on their way while the
+// The items of a pair, the same in every role.
+//
+// Whole items: pair p takes the items p, p + pairs, ... of B * max_tiles.
+//
+// Cut: every sequence's items weigh its last one's tiles and kLaItemCost; laid out in order their weights sum to
+// run_total, and pair p takes the places run_total * p / pairs .. run_total * (p + 1) / pairs.  Place x of an item is
+// its tile x - kLaItemCost (the first places are its own cost; tiles beyond the weight belong to the last place).
+struct LaIter {
+  uint32_t id, step, items;                 // whole items
+  int64_t pos, end, base;                   // cut: next place, end of the run, first place of sequence b
+  int b, n_items, weight;
+  bool any;
+  __device__ __forceinline__ LaIter(const LatentAttnParams& P, const LaBars* bars) {
+    id = blockIdx.x >> 1;
+    step = gridDim.x >> 1;
+    items = static_cast<uint32_t>(P.B) * P.max_tiles;   // below 2^30
+    any = false;
+    n_items = weight = 0;
+    if (P.cut) {
+      pos = bars->run_pos;
+      end = bars->run_end;
+      base = bars->run_base;
+      b = bars->run_seq;
+    } else {
+      pos = end = base = 0;
+      b = 0;
+    }
+  }
+  __device__ __forceinline__ bool next(const LatentAttnParams& P, bool tell, LaItem& w) {
+    int all;
+    if (!P.cut) {
+      for (; id < items; id += step) {
+        const uint32_t max_tiles = P.max_tiles;
+        const int seq = static_cast<int>(id / max_tiles);
+        if (la_item(P, seq, static_cast<int>(id - seq * max_tiles), tell, w, all)) {
+          id += step;
+          return true;
+        }
+      }
+      return false;
+    }
+    if (pos >= end) return false;
+    while (!any || pos >= base + static_cast<int64_t>(n_items) * weight) {   // the sequence of the next place
+      if (any) {
+        base += static_cast<int64_t>(n_items) * weight;
+        ++b;
+      }
+      if (b >= P.B) return false;
+      any = true;
+      const bool has = la_item(P, b, -1, false, w, all);
+      n_items = has ? all : 0;
+      weight = has ? w.nt + kLaItemCost : 0;
+    }
+    const int64_t at = pos - base;
+    const int64_t q = at / weight;
+    const int x0 = static_cast<int>(at - q * weight);
+    const int x1 = end - pos < weight - x0 ? x0 + static_cast<int>(end - pos) : weight;
+    la_item(P, b, static_cast<int>(q), false, w, all);
+    const int n = w.nt;
+    int i0 = x0 - kLaItemCost, i1 = x1 - kLaItemCost;
+    i0 = i0 < 0 ? 0 : i0 < n ? i0 : n;
+    i1 = x1 == weight ? n : i1 < 0 ? 0 : i1 < n ? i1 : n;
+    w.i0 = i0;
+    w.nt = i1 - i0;
+    if (x0 > 0 || x1 < weight) w.part = 2 * static_cast<int>(blockIdx.x >> 1) + (x0 > 0 ? 0 : 1);
+    pos += x1 - x0;
+    return true;
+  }
+};
+
+// Item `ic` of the CTA, copied out of shared memory by a warp, which gives its place back at once.
+__device__ __forceinline__ bool la_next_item(LaBars* bars, int ic, LaItem& w, volatile int* abort_flag) {
+  const int slot = ic % kLaItems;
+  if (!warp_wait<false>(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) return false;
+  w = bars->item[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[slot]);
+  return true;
+}
+
+// The pair's run of the cut form (one warp of each CTA).
+__device__ __forceinline__ void la_plan(const LatentAttnParams& P, LaBars* bars, int lane) {
+  const int64_t p = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  int64_t total = 0, lo = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < P.B && !found; b0 += 32) {
+      const int b = b0 + lane;
+      int64_t mine = 0;
+      if (b < P.B) {
+        LaItem w;
+        int all;
+        if (la_item(P, b, -1, pass == 0 && blockIdx.x == 0, w, all))
+          mine = static_cast<int64_t>(all) * (w.nt + kLaItemCost);
+      }
+      int64_t upto = mine;                            // with the sequences before it in this group of 32
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const int64_t group = __shfl_sync(0xffffffffu, upto, 31);
+      if (pass == 1) {
+        const uint32_t in = __ballot_sync(0xffffffffu, lo < before + upto);
+        if (in) {
+          found = true;
+          const int first = __ffs(in) - 1;
+          if (lane == first) {
+            bars->run_seq = b;
+            bars->run_base = before + upto - mine;
+          }
+        }
+      }
+      before += group;
+    }
+    if (pass == 0) {
+      total = before;
+      lo = total * p / pairs;
+      if (lane == 0) {
+        bars->run_total = total;
+        bars->run_pos = lo;
+        bars->run_end = total * (p + 1) / pairs;
+        bars->run_seq = P.B;                          // nothing to do unless the second pass finds the place
+        bars->run_base = 0;
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// Persistent: the roles run through the pair's items (LaIter) at their own pace: the next item's query, first tiles and logits are on their way while the
 // output of the last one leaves.  Barrier phases follow counts that run on over the items: tiles (g), items with
 // tiles (qn), exchanges (xn).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
-  extern __shared__ uint8_t la_raw[];
-  uint8_t* smem = smem_align1024(la_raw);
+  extern __shared__ __align__(1024) uint8_t la_raw[];
+  uint8_t* smem = la_raw;
+  if (smem_u32(smem) & 1023u) {                       // the swizzle needs what the declaration asks for
+    if (threadIdx.x == 0) atomicOr(&g_fault, FAULT_WAIT_TIMEOUT);
+    return;
+  }
   LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);
   volatile int* abort_flag = &bars->abort_flag;
   // (broadcasts of what is the same in a warp anyway let the compiler keep it, and the MMAs' operands, uniform: an
@@ -406,16 +557,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int cr = static_cast<int>(blockIdx.x & 1);    // rank in the pair
-  const uint32_t items = static_cast<uint32_t>(P.B) * P.max_tiles * P.n_split;   // below 2^30
-  const uint32_t item0 = blockIdx.x >> 1, item_step = gridDim.x >> 1;
   const int H = P.H;
   const bool is_tree = P.tree != nullptr;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->qfull, 1);
     mbar_init(&bars->q_empty, 1);
-    mbar_init(&bars->k_full, kLaKGroups);
-    for (int g = 0; g < kLaKGroups; ++g) mbar_init(&bars->k_empty[g], 1);
+    for (int g = 0; g < kLaKGroups; ++g) {
+      mbar_init(&bars->k_full[g], 1);
+      mbar_init(&bars->k_empty[g], 1);
+    }
     mbar_init(&bars->v_seen, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bars->v_full[g], 1);
@@ -425,6 +576,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       mbar_init(&bars->mx[g], 2);
     }
     mbar_init(&bars->pfull, 8);
+    for (int i = 0; i < kLaItems; ++i) {
+      mbar_init(&bars->item_full[i], 1);
+      mbar_init(&bars->item_empty[i], 7);             // every warp but the one that writes them
+    }
     mbar_init(&bars->odone, 1);
     mbar_init(&bars->drain[0], 1);
     mbar_init(&bars->drain[1], 1);
@@ -437,6 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  if (warp == 2 && P.cut) la_plan(P, bars, lane);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&M.q);
     tma_prefetch_desc(&M.k);
@@ -449,70 +605,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ copies
+    // ------------------------------------------------------------ query and key copies
     // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).
     if (lane == 0) {
       const bool first = cr == 0;
-      const uint32_t qfull = la_map(&bars->qfull, 0), k_full = la_map(&bars->k_full, 0);
-      const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
+      const uint32_t qfull = la_map(&bars->qfull, 0);
+      const uint32_t k_full[3] = {la_map(&bars->k_full[0], 0), la_map(&bars->k_full[1], 0), la_map(&bars->k_full[2], 0)};
       bool ok = true;
       int g = 0, qn = 0;
-      for (uint32_t id = item0; id < items && ok; id += item_step) {
+      LaIter it(P, bars);
+      LaJoin join{0, 0, 0};
+      for (int ic = 0; ok; ++ic) {
         LaItem w;
-        if (!la_item(P, id, first, w) || w.nt == 0) continue;
+        if (!it.next(P, first, w)) w.nt = -1;
+        const int slot = ic % kLaItems;
+        if (!mbar_wait<false>(&bars->item_empty[slot], ((ic / kLaItems) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        bars->item[slot] = w;
+        mbar_arrive(&bars->item_full[slot]);
+        if (w.nt < 0) break;
+        if (w.part >= 0 && (w.part & 1)) {            // begins in this run and goes on in the next pairs'
+          const int64_t pairs = gridDim.x >> 1, item_end = it.base + ((it.pos - 1 - it.base) / it.weight + 1) * it.weight;
+          int64_t k = (blockIdx.x >> 1) + 1;
+          while (k < pairs && bars->run_total * k / pairs < item_end) ++k;
+          join.row0 = w.grow0;
+          join.nrows = w.nrows;
+          join.parts = static_cast<int>(k - (blockIdx.x >> 1));
+        }
+        if (w.nt == 0) continue;
         if (!mbar_wait<false>(&bars->q_empty, (qn & 1) ^ 1, abort_flag)) { ok = false; break; }
         ++qn;
         if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
         for (int c = 0; c < kLaKGroups; ++c)
-          la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, static_cast<int>(w.grow0 + kLaHalf * cr),
-                     kLaKPer * c);
-        // keys of tile i, then values of tile i - 1: the order in which their places become free
-        for (int i = 0; i <= w.nt && ok; ++i) {
-          if (i < w.nt) {
-            int kind, a, cnt;
-            w.sp.tile(w.i0 + i, kind, a, cnt);
-            const int box = la_box_rows(cnt) / 2;     // this CTA's half of the rows
-            const int row = static_cast<int>(w.off + a + (kind ? w.kv : 0)) + box * cr;
-            for (int c = 0; c < kLaKGroups; ++c) {
-              if (!mbar_wait<false>(&bars->k_empty[c], ((g + i) & 1) ^ 1, abort_flag)) { ok = false; break; }
-              if (first) mbar_arrive_expect_tx(&bars->k_full, 2 * kLaKPer * box * 128);
-              la_load_3d(smem + kLaOffK + c * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full, row,
-                         kLaKPer * c);
-            }
-          }
-          if (i > 0 && ok) {
-            const int j = i - 1;
-            int kind, a, cnt;
-            w.sp.tile(w.i0 + j, kind, a, cnt);
-            const int box = la_box_rows(cnt);
-            const int row = static_cast<int>(w.off + a + (kind ? w.kv : 0));
-            for (int c = 0; c < 2; ++c) {
-              // output MMA c has value columns 256 c .. : this CTA's 128 are panels 4 c + 2 cr and the next
-              if (!mbar_wait<false>(&bars->v_empty[c], ((g + j) & 1) ^ 1, abort_flag)) { ok = false; break; }
-              if (first) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
-              la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
-                         4 * c + 2 * cr);
-            }
+          la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, w.grow0 + kLaHalf * cr, kLaKPer * c);
+        for (int i = 0; i < w.nt && ok; ++i) {
+          int kind, a, cnt;
+          w.sp.tile(w.i0 + i, kind, a, cnt);
+          const int box = la_box_rows(cnt) / 2;       // this CTA's half of the rows
+          const int row = (kind ? w.rowd : w.row0) + a + box * cr;
+#pragma unroll
+          for (int c = 0; c < kLaKGroups; ++c) {
+            if (!mbar_wait<false>(&bars->k_empty[c], ((g + i) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (first) mbar_arrive_expect_tx(&bars->k_full[c], 2 * kLaKPer * box * 128);
+            la_load_3d(smem + kLaOffK + c * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full[c], row,
+                       kLaKPer * c);
           }
         }
         g += w.nt;
       }
-      if (!ok) {
-        // after an abort: the copies in flight (microseconds) land before the CTA ends
-        const uint64_t t = globaltimer_ns();
-        while (globaltimer_ns() - t < 1000000ull) __nanosleep(1000);
+      if (P.cut && first) P.joins[blockIdx.x >> 1] = join;
+      if (!ok) la_settle();
+    }
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ value copies
+    // (a warp of their own: their places become free at another pace than the keys')
+    if (lane == 0) {
+      const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
+      bool ok = true;
+      int g = 0;
+      for (int ic = 0; ok; ++ic) {
+        const int slot = ic % kLaItems;
+        if (!mbar_wait<false>(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) { ok = false; break; }
+        const LaItem w = bars->item[slot];
+        mbar_arrive(&bars->item_empty[slot]);
+        if (w.nt < 0) break;
+        for (int i = 0; i < w.nt && ok; ++i, ++g) {
+          int kind, a, cnt;
+          w.sp.tile(w.i0 + i, kind, a, cnt);
+          const int box = la_box_rows(cnt);
+          const int row = (kind ? w.rowd : w.row0) + a;
+          for (int c = 0; c < 2; ++c) {
+            // output MMA c has value columns 256 c .. : this CTA's 128 are panels 4 c + 2 cr and the next
+            if (!mbar_wait<false>(&bars->v_empty[c], (g & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (cr == 0) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
+            la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
+                       4 * c + 2 * cr);
+          }
+        }
       }
+      if (!ok) la_settle();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ logit MMAs of the pair (first CTA)
     const uint32_t base = smem_u32(smem);
     const uint64_t qdesc = sw128_kmajor_desc(base), kdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffK));
-    bool ok = cr == 0;
+    bool ok = true;
     int g = 0, qn = 0;
-    for (uint32_t id = item0; id < items && ok; id += item_step) {
+    for (int ic = 0; ok; ++ic) {
       LaItem w;
-      if (!la_item(P, id, false, w) || w.nt == 0) continue;
+      if (!la_next_item(bars, ic, w, abort_flag)) { ok = false; break; }
       const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+      if (nt < 0) break;
+      if (nt == 0 || cr == 1) continue;               // the first CTA issues for both
       if (!la_wait_all(&bars->qfull, qn & 1, abort_flag)) { ok = false; break; }
       ++qn;
       for (int i = 0; i < nt; ++i, ++g) {
@@ -520,33 +703,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         w.sp.tile(w.i0 + i, kind, a, cnt);
         const bool full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
         const uint32_t d = tmem + kLaColS + 64 * (g & 1);
-        if (!la_wait_all(&bars->s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort_flag) ||
-            !la_wait_all(&bars->k_full, g & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        // the two sizes apart, so that every descriptor is a constant away from one of two
-        if (full) {
-#pragma unroll
-          for (int p = 0; p < kLaPanels; ++p) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              la_mma(d, qdesc + (p * kLaPanelBytes + 32 * kk) / 16, kdesc + (p * kLaPanelBytes + 32 * kk) / 16,
-                     idesc_bf16_f32(kLaRows, kLaTile), (p | kk) ? 1u : 0u);
-            if (p % kLaKPer == kLaKPer - 1) la_commit_both(&bars->k_empty[p / kLaKPer]);
-          }
-        } else {
-          // few rows: a group's panels lie 16 rows apart
+        if (!la_wait_all(&bars->s_empty[g & 1], ((g >> 1) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        // the two sizes apart, so that a descriptor is a constant away from one per group; loops over the groups, for
+        // the instruction cache's sake
 #pragma unroll 1
-          for (int c = 0; c < kLaKGroups; ++c) {
-#pragma unroll 1
+        for (int c = 0; c < kLaKGroups; ++c) {
+          if (!la_wait_all(&bars->k_full[c], g & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t qd = qdesc + c * (kLaKPer * kLaPanelBytes / 16), kd = kdesc + c * (kLaKPer * kLaPanelBytes / 16);
+          const uint32_t acc0 = c ? 1u : 0u;
+          if (full) {
+#pragma unroll
             for (int p = 0; p < kLaKPer; ++p)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                la_mma(d, qdesc + ((c * kLaKPer + p) * kLaPanelBytes + 32 * kk) / 16,
-                       kdesc + (c * kLaKPer * kLaPanelBytes + p * (kLaFew * 64) + 32 * kk) / 16,
-                       idesc_bf16_f32(kLaRows, kLaFew), (c | p | kk) ? 1u : 0u);
-            la_commit_both(&bars->k_empty[c]);
+                la_mma(d, qd + (p * kLaPanelBytes + 32 * kk) / 16, kd + (p * kLaPanelBytes + 32 * kk) / 16,
+                       idesc_bf16_f32(kLaRows, kLaTile), (p | kk) ? 1u : acc0);
+          } else {
+            // few rows: a group's panels lie 16 rows apart
+#pragma unroll
+            for (int p = 0; p < kLaKPer; ++p)
+#pragma unroll 1
+              for (int kk = 0; kk < 4; ++kk)
+                la_mma(d, qd + (p * kLaPanelBytes + 32 * kk) / 16, kd + (p * (kLaFew * 64) + 32 * kk) / 16,
+                       idesc_bf16_f32(kLaRows, kLaFew), (p | kk) ? 1u : acc0);
           }
+          la_commit_both(&bars->k_empty[c]);
         }
+        if (!ok) break;
         la_commit_both(&bars->sfull[g & 1]);
         if (i == nt - 1) la_commit_both(&bars->q_empty);
       }
@@ -565,13 +749,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
                    vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
                    vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
     const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
-    bool ok = cr == 0;
+    bool ok = true;
     int g = 0;
-    for (uint32_t id = item0; id < items && ok; id += item_step) {
+    for (int ic = 0; ok; ++ic) {
       LaItem w;
-      if (!la_item(P, id, false, w)) continue;
+      if (!la_next_item(bars, ic, w, abort_flag)) { ok = false; break; }
       const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
-      for (int i = 0; i < nt; ++i, ++g) {
+      if (nt < 0) break;
+      for (int i = 0; i < nt && cr == 0; ++i, ++g) {  // the first CTA issues for both
         int kind, a, cnt;
         w.sp.tile(w.i0 + i, kind, a, cnt);
         const bool full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
@@ -587,22 +772,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         if (!la_wait_all(&bars->pfull, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t acc0 = i ? 1u : 0u;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           if (c == 1) {
             if (!la_wait_all(&bars->v_full[1], g & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
           }
           const uint32_t d = tmem + kLaColO + 128 * c;
+          const uint64_t vd = vdesc + c * (kLaVGroup / 16), vf = vdesc_few + c * (kLaVGroup / 16);
           if (full) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vdesc + (c * kLaVGroup + 2048 * s) / 16,
+              la_mma(d, pdesc + ((s >> 2) * kLaPanelBytes + 32 * (s & 3)) / 16, vd + 2048 * s / 16,
                      idesc_o, s ? 1u : acc0);
           } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-              la_mma(d, pdesc + 32 * s / 16, vdesc_few + (c * kLaVGroup + 2048 * s) / 16, idesc_o, s ? 1u : acc0);
+              la_mma(d, pdesc + 32 * s / 16, vf + 2048 * s / 16, idesc_o, s ? 1u : acc0);
           }
           la_commit_both(&bars->v_empty[c]);
         }
@@ -625,18 +811,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + kLaOffX);
     const uint32_t pfull0 = la_map(&bars->pfull, 0);
-    // logits in log2 units; below 0 the logits' signs are turned instead
-    const bool turn = P.scale < 0.f;
-    const float sl2 = fabsf(P.scale) * 1.4426950408889634f;
+    // a pair without a run (fewer places than pairs) may lie between an item's parts: its own is empty
+    if (P.cut && cr == 0 && bars->run_pos == bars->run_end)
+      P.part_lse[2 * static_cast<int64_t>(blockIdx.x >> 1) * kLaRows + tl] = neg_inf();
+    // logits in log2 units; a scale that is not above 0 turns (or clears) the logits first
+    const bool turn = !(P.scale > 0.f);
+    const float mult = P.scale < 0.f ? -1.f : 0.f;
+    const float sl2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
     bool ok = true;
     const uint32_t s_read[2] = {la_map(&bars->s_empty[0], 0), la_map(&bars->s_empty[1], 0)};
     float* xsum = reinterpret_cast<float*>(smem + kLaOffL);
     int g = 0, xn = 0, vn = 0;                        // tiles, exchanges, tiles that are not whole
-    for (uint32_t id = item0; id < items && ok; id += item_step) {
+    for (int ic = 0; ok; ++ic) {
     LaItem w;
-    if (!la_item(P, id, false, w)) continue;
+    if (!la_next_item(bars, ic, w, abort_flag)) { ok = false; break; }
     const LaSpan& sp = w.sp;
     const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+    if (nt < 0) break;
     const bool live = rq < w.nrows;
     const int tok = (static_cast<uint32_t>(w.r0) + (live ? rq : w.nrows - 1)) / static_cast<uint32_t>(H);
     // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
@@ -687,14 +878,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       if (turn) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          va[j] ^= 0x80000000u;
-          vb[j] ^= 0x80000000u;
+          va[j] = __float_as_uint(__uint_as_float(va[j]) * mult);
+          vb[j] = __float_as_uint(__uint_as_float(vb[j]) * mult);
         }
       }
       if (!whole) {
-        const uint64_t there = la_low_mask(hs);
-        const bool bad = la_mask_row(va, static_cast<uint32_t>(vis), static_cast<uint32_t>(there)) |
-                         la_mask_row(vb, static_cast<uint32_t>(vis >> 32), static_cast<uint32_t>(there >> 32));
+        const bool bad = la_mask_row(va, static_cast<uint32_t>(vis)) | la_mask_row(vb, static_cast<uint32_t>(vis >> 32));
         // A cache row that holds something not finite gives every query row of the pair a logit that is not
         // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
         // arrival (two warps that clear the same piece store the same bytes).
@@ -735,15 +924,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       lt *= f;
       const float ref = m == neg_inf() ? 0.f : m;
       uint32_t pw[32];
-      if (whole)
-        la_row_weights<false>(va, vb, vis, sl2, ref, pw, l, lt);
-      else
-        la_row_weights<true>(va, vb, vis, sl2, ref, pw, l, lt);
+      la_row_weights(va, vb, sl2, ref, pw, l, lt);
       if (i > 0) {
         // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
         if (!warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[32];
             tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
@@ -791,13 +978,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       // nothing visible (or only -inf logits): the sum of the rounded weights is 0 exactly when that of the weights is
       const bool empty = lt == 0.f;
       const float inv = empty ? 0.f : 1.f / lt;
-      const int64_t row = w.grow0 + rq;
-      const bool parts = P.n_split > 1;
-      const int64_t part0 = static_cast<int64_t>(w.split) * P.T * H;
+      const int64_t row = static_cast<int64_t>(w.grow0) + rq;
+      const bool parts = w.part >= 0;
+      const int64_t part_row = static_cast<int64_t>(w.part) * kLaRows + rq;
       if (half == 0 && live) {
         const float v = empty ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
         if (parts)
-          P.part_lse[part0 + row] = v;
+          P.part_lse[part_row] = v;
         else if (P.lse)
           P.lse[row] = v;
       }
@@ -806,47 +993,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       // value columns 256 (c / 4) + 128 half + 32 (c % 4) ...
       const bool wide = parts || !P.out_bf16;
       const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
-      const int64_t row0 = w.grow0 + kLaHalf * cr + (quad & 1) * 32;                 // first row of the warp
-      uint8_t* dst = parts ? reinterpret_cast<uint8_t*>(P.part_o + part0 * kAttnValue) : static_cast<uint8_t*>(P.out);
+      const int64_t row0 = (parts ? static_cast<int64_t>(w.part) * kLaRows : static_cast<int64_t>(w.grow0)) + kLaHalf * cr + (quad & 1) * 32;
+      uint8_t* dst = parts ? reinterpret_cast<uint8_t*>(P.part_o) : static_cast<uint8_t*>(P.out);
       dst += row0 * (kAttnValue * (wide ? 4 : 2));
       uint8_t* stage = smem + kLaOffP + quad * 4096;
       uint8_t* mine = stage + lane * 128;
+      // (rolled loops: this code runs once an item, and what it takes of the instruction cache the tiles' code misses)
 #pragma unroll 1
-      for (int c = 0; c < 8; c += 2) {
-        uint32_t x[2][32];
+      for (int c = 0; c < 8; ++c) {
+        uint32_t x[32];
         if (nt > 0) {
-          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x[0]);
-          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c + 32, x[1]);
-          tmem_wait_ld(x[0]);
-          tmem_wait_ld(x[1]);
+          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x);
+          tmem_wait_ld(x);
         }
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int k = 0; k < 32; ++k) x[k] = empty ? 0u : __float_as_uint(__uint_as_float(x[k]) * inv);
+        if (wide) {                                   // 32 columns are 128 bytes
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[u][k] = empty ? 0u : __float_as_uint(__uint_as_float(x[u][k]) * inv);
-          if (wide) {                                 // 32 columns are 128 bytes
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
+                make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        } else {                                      // 64 columns are
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
-                  make_uint4(x[u][4 * k], x[u][4 * k + 1], x[u][4 * k + 2], x[u][4 * k + 3]);
-            la_rows_out(stage, dst + 4 * (col + 32 * u), kAttnValue * 4, keep, lane);
-          } else {                                    // 64 columns are
+          for (int k = 0; k < 4; ++k) {
+            uint32_t p2[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t p2[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(x[u][8 * k + 2 * e]),
-                                                               __uint_as_float(x[u][8 * k + 2 * e + 1]));
-                p2[e] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              *reinterpret_cast<uint4*>(mine + (((k + 4 * u) ^ (lane & 7)) << 4)) =
-                  make_uint4(p2[0], p2[1], p2[2], p2[3]);
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 h =
+                  __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]), __uint_as_float(x[8 * k + 2 * e + 1]));
+              p2[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            *reinterpret_cast<uint4*>(mine + (((k + 4 * (c & 1)) ^ (lane & 7)) << 4)) =
+                make_uint4(p2[0], p2[1], p2[2], p2[3]);
           }
         }
-        if (!wide) la_rows_out(stage, dst + 2 * col, kAttnValue * 2, keep, lane);
+        if (wide || (c & 1))
+          la_rows_out(stage, dst + (wide ? 4 * col : 2 * (col - 32)), kAttnValue * (wide ? 4 : 2), keep, lane);
       }
     }
     }
@@ -862,75 +1045,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   }
 }
 
-// Joins the parts of the split form: a block of 128 threads per row, four
-// value columns a thread; parts whose lse is -inf are not read.  Rows behind
-// the last sequence are left as they were.
+// Joins the parts of the items that cuts went through: blockIdx.x is the pair whose run the item begins in, its part
+// 2 p + 1, the next pairs' parts 2 (p + 1), ...; blockIdx.y takes 4 of its rows, four value columns a thread.  Parts
+// whose lse is -inf are not read.
 __global__ void __launch_bounds__(128)
     latent_attn_combine_kernel(const __grid_constant__ LatentAttnParams P) {
-  const int64_t row = blockIdx.x;
-  const int64_t rows = static_cast<int64_t>(P.T) * P.H;
-  const int last = __ldg(P.q_start + P.B);
-  if (row < static_cast<int64_t>(__ldg(P.q_start)) * P.H || row >= static_cast<int64_t>(last) * P.H) return;
-  float m = neg_inf();
-  for (int s = 0; s < P.n_split; ++s) m = fmaxf(m, __ldg(P.part_lse + s * rows + row));
-  float den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < P.n_split; ++s) {
-    const float ls = __ldg(P.part_lse + s * rows + row);
-    if (ls == neg_inf()) continue;
-    const float w = expf(ls - m);
-    const float4 v = __ldg(reinterpret_cast<const float4*>(P.part_o + (s * rows + row) * kAttnValue) + threadIdx.x);
-    den += w;
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  if (threadIdx.x == 0 && P.lse) P.lse[row] = den == 0.f ? neg_inf() : m + logf(den);
-  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (P.out_bf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), c = __floats2bfloat162_rn(o.z, o.w);
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * kAttnValue)[threadIdx.x] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-  } else {
-    reinterpret_cast<float4*>(static_cast<float*>(P.out) + row * kAttnValue)[threadIdx.x] = o;
+  const int p = blockIdx.x;
+  const LaJoin join = P.joins[p];
+  for (int r = 4 * blockIdx.y; r < 4 * blockIdx.y + 4 && r < join.nrows && join.parts > 0; ++r) {
+    const auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * p + 1 : 2 * (p + k)) * kLaRows + r; };
+    float m = neg_inf();
+    for (int k = 0; k < join.parts; ++k) m = fmaxf(m, __ldg(P.part_lse + at(k)));
+    float den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < join.parts; ++k) {
+      const float ls = __ldg(P.part_lse + at(k));
+      if (ls == neg_inf()) continue;
+      const float w = expf(ls - m);
+      const float4 v = __ldg(reinterpret_cast<const float4*>(P.part_o + at(k) * kAttnValue) + threadIdx.x);
+      den += w;
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const int64_t row = join.row0 + r;
+    if (threadIdx.x == 0 && P.lse) P.lse[row] = den == 0.f ? neg_inf() : m + logf(den);
+    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (P.out_bf16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), c = __floats2bfloat162_rn(o.z, o.w);
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * kAttnValue)[threadIdx.x] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+    } else {
+      reinterpret_cast<float4*>(static_cast<float*>(P.out) + row * kAttnValue)[threadIdx.x] = o;
+    }
   }
 }
 
-cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, int num_sms, cudaStream_t st) {
+cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = smem_limit_once(attr_done, reinterpret_cast<const void*>(&latent_attn_kernel), kLaSmem);
   if (e != cudaSuccess) return e;
-  const int64_t items = static_cast<int64_t>(p.B) * p.max_tiles * p.n_split;
-  const int64_t pairs = items < num_sms / 2 ? items : num_sms / 2;
-  latent_attn_kernel<<<static_cast<unsigned>(2 * pairs), kLaThreads, kLaSmem, st>>>(maps, p);
+  latent_attn_kernel<<<static_cast<unsigned>(2 * p.pairs), kLaThreads, kLaSmem, st>>>(maps, p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_latent_attn_combine(const LatentAttnParams& p, cudaStream_t st) {
-  latent_attn_combine_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.T) * p.H), 128, 0, st>>>(p);
+  latent_attn_combine_kernel<<<dim3(static_cast<unsigned>(p.pairs), kLaRows / 4), 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 
-// Number of CTA pairs that share one tile of query rows.  `pairs` pairs cover
-// the query rows, each over at most `tiles` tiles of the cache; the machine
-// runs 74 pairs at once.  A tile costs about 1.4 us, a pair about 5 tiles more
-// for its query, its first copies and its output, and the combine about 3
-// (with the launch): the split that makes the longest chain shortest.
-inline int la_splits(int64_t pairs, int64_t tiles) {
-  int best = 1;
-  int64_t best_cost = 0;
-  const int64_t most = tiles < kLaMaxSplit ? tiles : kLaMaxSplit;
-  for (int64_t s = 1; s <= (most > 1 ? most : 1); ++s) {
-    const int64_t waves = (pairs * s + 73) / 74;
-    const int64_t cost = waves * ((tiles + s - 1) / s + 5) + (s > 1 ? 3 : 0);
-    if (s == 1 || cost < best_cost) {
-      best = static_cast<int>(s);
-      best_cost = cost;
-    }
-  }
-  return best;
+// How the work is laid out, from what the host knows: at most `items` items of at most `tiles` tiles.  Whole items in
+// turn unless equal runs are shorter by more than 15 percent and the join's cost (about 4 tiles: a launch and the
+// parts' way through memory).  74 pairs run at once.
+struct LaLayout {
+  int pairs, cut;
+};
+inline LaLayout la_layout(int64_t items, int64_t tiles) {
+  constexpr int64_t kPairs = 74;
+  const int64_t weight = tiles + kLaItemCost, total = items * weight;
+  const int64_t whole = (items + kPairs - 1) / kPairs * weight;
+  const int64_t runs = total < kPairs ? total : kPairs;
+  const int64_t cut = (total + runs - 1) / runs + 4;
+  LaLayout l;
+  l.cut = 100 * whole > 115 * cut;
+  l.pairs = static_cast<int>(l.cut ? runs : items < kPairs ? items : kPairs);
+  return l;
 }
 
 }  // namespace lsi
