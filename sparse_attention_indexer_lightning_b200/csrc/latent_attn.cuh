@@ -209,12 +209,26 @@ __device__ __forceinline__ void la_settle() {
 // Rows of a tile as it is staged.
 __device__ __forceinline__ int la_box_rows(int cnt) { return cnt <= kLaFew ? kLaFew : kLaTile; }
 
+// Warp-uniform bounded wait of lane 0.  What the other lanes do in shared memory behind it is kept there: by a compiler
+// barrier where they write (the vote holds them until lane 0 has seen the phase), by a warp barrier, which also orders
+// memory, where they read what other warps wrote (la_wait_read; without it they met the old values now and then).
+__device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = warp_wait<false>(bar, parity, abort_flag);
+  asm volatile("" ::: "memory");
+  return ok;
+}
+__device__ __forceinline__ bool la_wait_read(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = warp_wait<false>(bar, parity, abort_flag);
+  __syncwarp();
+  return ok;
+}
+
 // Warp-uniform bounded wait in which every lane tests the barrier: when the
 // phase is complete already, the common case of the MMA warp, it costs one
 // test and a vote.
 __device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait(bar, parity, abort_flag);
+  return la_wait(bar, parity, abort_flag);
 }
 
 // Address of this CTA's shared-memory object in CTA `rank` of the cluster, and an arrival there.  What the arrival
@@ -481,7 +495,7 @@ struct LaIter {
 // Item `ic` of the CTA, copied out of shared memory by a warp, which gives its place back at once.
 __device__ __forceinline__ bool la_next_item(LaBars* bars, int ic, LaItem& w, volatile int* abort_flag) {
   const int slot = ic % kLaItems;
-  if (!warp_wait<false>(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) return false;
+  if (!la_wait_read(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) return false;
   w = bars->item[slot];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[slot]);
@@ -864,7 +878,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         else
           vis = cnt > 0 ? (__ldg(branch + (a >> 6)) >> (a & 63)) & la_low_mask(cnt) : 0ull;
       }
-      if (!warp_wait<false>(&bars->sfull[st], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+      if (!la_wait(&bars->sfull[st], (g >> 1) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
       uint32_t va[32], vb[32];
       const uint32_t scol = trow + kLaColS + 64 * st;
@@ -888,8 +902,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
         // arrival (two warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
-          if ((i > 0 && !warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) ||
-              !warp_wait<false>(&bars->v_seen, vn & 1, abort_flag)) {
+          if ((i > 0 && !la_wait(&bars->odone, (g - 1) & 1, abort_flag)) ||
+              !la_wait_read(&bars->v_seen, vn & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -914,7 +928,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       xch[128 * st + tl] = mt;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      if (!warp_wait<false>(&bars->mx[grp], xn & 1, abort_flag)) { ok = false; break; }
+      if (!la_wait_read(&bars->mx[grp], xn & 1, abort_flag)) { ok = false; break; }
       ++xn;
       mt = fmaxf(mt, xch[128 * st + (tl ^ 64)]);
       const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
@@ -927,7 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       la_row_weights(va, vb, sl2, ref, pw, l, lt);
       if (i > 0) {
         // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
-        if (!warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
+        if (!la_wait(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
@@ -961,7 +975,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       if (lane == 0) la_arrive_at(pfull0);
     }
     // ------------------------------------------------------------ output
-    if (ok && nt > 0) ok = warp_wait<false>(&bars->odone, (g - 1) & 1, abort_flag);
+    if (ok && nt > 0) ok = la_wait(&bars->odone, (g - 1) & 1, abort_flag);
     if (ok && nt > 0) {
       // the row's sums: the two threads' halves
       tc_fence_after();
@@ -969,7 +983,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       if (half) xsum[128 + r] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      ok = warp_wait<false>(&bars->mx[grp], xn & 1, abort_flag);
+      ok = la_wait_read(&bars->mx[grp], xn & 1, abort_flag);
       ++xn;
       lt += xsum[tl ^ 64];
       if (!half) l += xsum[128 + r];
@@ -1046,40 +1060,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
 }
 
 // Joins the parts of the items that cuts went through: blockIdx.x is the pair whose run the item begins in, its part
-// 2 p + 1, the next pairs' parts 2 (p + 1), ...; blockIdx.y takes 4 of its rows, four value columns a thread.  Parts
+// 2 p + 1, the next pairs' parts 2 (p + 1), ...; blockIdx.y is one of its rows, four value columns a thread.  Parts
 // whose lse is -inf are not read.
 __global__ void __launch_bounds__(128)
     latent_attn_combine_kernel(const __grid_constant__ LatentAttnParams P) {
-  const int p = blockIdx.x;
+  __shared__ float s_lse[128];                        // at most 74 pairs
+  const int p = blockIdx.x, r = blockIdx.y;
   const LaJoin join = P.joins[p];
-  for (int r = 4 * blockIdx.y; r < 4 * blockIdx.y + 4 && r < join.nrows && join.parts > 0; ++r) {
-    const auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * p + 1 : 2 * (p + k)) * kLaRows + r; };
-    float m = neg_inf();
-    for (int k = 0; k < join.parts; ++k) m = fmaxf(m, __ldg(P.part_lse + at(k)));
-    float den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < join.parts; ++k) {
-      const float ls = __ldg(P.part_lse + at(k));
-      if (ls == neg_inf()) continue;
-      const float w = expf(ls - m);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(P.part_o + at(k) * kAttnValue) + threadIdx.x);
-      den += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
-    }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
-    const int64_t row = join.row0 + r;
-    if (threadIdx.x == 0 && P.lse) P.lse[row] = den == 0.f ? neg_inf() : m + logf(den);
-    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (P.out_bf16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), c = __floats2bfloat162_rn(o.z, o.w);
-      reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * kAttnValue)[threadIdx.x] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
-    } else {
-      reinterpret_cast<float4*>(static_cast<float*>(P.out) + row * kAttnValue)[threadIdx.x] = o;
-    }
+  if (r >= join.nrows || join.parts <= 0) return;
+  const auto at = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * p + 1 : 2 * (p + k)) * kLaRows + r; };
+  const int parts = join.parts < 128 ? join.parts : 128;
+  if (threadIdx.x < parts) s_lse[threadIdx.x] = __ldg(P.part_lse + at(threadIdx.x));
+  __syncthreads();
+  float m = neg_inf();
+  for (int k = 0; k < parts; ++k) m = fmaxf(m, s_lse[k]);
+  float den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k) {
+    const float ls = s_lse[k];
+    if (ls == neg_inf()) continue;
+    const float w = expf(ls - m);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(P.part_o + at(k) * kAttnValue) + threadIdx.x);
+    den += w;
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int64_t row = join.row0 + r;
+  if (threadIdx.x == 0 && P.lse) P.lse[row] = den == 0.f ? neg_inf() : m + logf(den);
+  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (P.out_bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), c = __floats2bfloat162_rn(o.z, o.w);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(P.out) + row * kAttnValue)[threadIdx.x] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+  } else {
+    reinterpret_cast<float4*>(static_cast<float*>(P.out) + row * kAttnValue)[threadIdx.x] = o;
   }
 }
 
@@ -1092,12 +1110,12 @@ cudaError_t launch_latent_attn(const LaMaps& maps, const LatentAttnParams& p, cu
 }
 
 cudaError_t launch_latent_attn_combine(const LatentAttnParams& p, cudaStream_t st) {
-  latent_attn_combine_kernel<<<dim3(static_cast<unsigned>(p.pairs), kLaRows / 4), 128, 0, st>>>(p);
+  latent_attn_combine_kernel<<<dim3(static_cast<unsigned>(p.pairs), kLaRows), 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 // How the work is laid out, from what the host knows: at most `items` items of at most `tiles` tiles.  Whole items in
-// turn unless equal runs are shorter by more than 15 percent and the join's cost (about 4 tiles: a launch and the
+// turn unless equal runs are shorter by more than 5 percent and the join's cost (about 4 tiles: a launch and the
 // parts' way through memory).  74 pairs run at once.
 struct LaLayout {
   int pairs, cut;
@@ -1109,7 +1127,7 @@ inline LaLayout la_layout(int64_t items, int64_t tiles) {
   const int64_t runs = total < kPairs ? total : kPairs;
   const int64_t cut = (total + runs - 1) / runs + 4;
   LaLayout l;
-  l.cut = 100 * whole > 115 * cut;
+  l.cut = 100 * whole > 105 * cut;
   l.pairs = static_cast<int>(l.cut ? runs : items < kPairs ? items : kPairs);
   return l;
 }

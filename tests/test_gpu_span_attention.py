@@ -279,6 +279,32 @@ def test_splits_agree_and_repeat(L):
         assert (z - runs[0][1]).abs().max() <= LOGIT
 
 
+@pytest.mark.parametrize("case", [WINDOWS[i] for i in (7, 9, 12, 15, 16)], ids=["7", "9", "12", "15", "16"])
+def test_every_call_gives_the_same_bits(L, case):
+    """300 calls, bit for bit: what one warp reads of another's maxima, sums and items has been written by then."""
+    ns, lens, H, w, align, sinks = case
+    d = make(ns, lens, H, seed=H)
+    args = (d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]))
+    kw = dict(row_off=dev(d["off"]), window=w, align=align, n_sink=sinks, out_dtype=torch.float32)
+    out, lse = L.ls_window_attention(*args, **kw)
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        o, z = L.ls_window_attention(*args, **kw)
+        bad += (o.view(torch.int32) != out.view(torch.int32)).sum() + (z.view(torch.int32) != lse.view(torch.int32)).sum()
+    assert int(bad) == 0
+
+
+def test_ragged_trees_cut_into_equal_runs(L):
+    """More items than pairs, of very different lengths: cuts go through many items, some items lie in one run and
+    some runs inside one item; one item's parts over all pairs; a sequence without tokens, one without rows."""
+    for ns, lens, H in (([9, 0, 1, 30, 2, 17], [2000, 50, 0, 300, 5000, 130], 128), ([1], [20000], 128),
+                        ([3, 3], [0, 9000], 24), ([100], [700], 128)):
+        d = make(ns, lens, H, "marks", seed=len(ns) + H, drafted=True)
+        branches = random_tree(d["rng"], ns)
+        tree(L, d, branches, "marks", dtype=torch.float32, max_ctx=max(lens))
+        tree(L, d, branches, "marks")
+
+
 def test_far_rows(L):
     """Rows more than 2^31 elements and 2^32 bytes into the cache."""
     R = 4_200_000
