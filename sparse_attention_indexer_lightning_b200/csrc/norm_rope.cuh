@@ -31,8 +31,11 @@
 namespace lsi {
 
 constexpr int kNrMaxDim = 1024;
-constexpr int kNrWarps = 4;
 constexpr int kNrMaxRope = 256;
+// Warps of a block.  What a block does once (the angles, a lane's part of them and of the weights) is worth more rows
+// where rows are short: 4096 x 33 rows of 128 elements take 26 us with two warps, 33 with four; 2048 x 129 rows of 576
+// elements 117 and 111.
+constexpr int nr_warps(int steps) { return steps == 1 ? 2 : 4; }
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
 struct NormRows {
@@ -71,26 +74,34 @@ __device__ __forceinline__ float nr_row_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ void nr_load8(float (&w)[8], const float* __restrict__ p) {
+// Elements c .. c + 7 of a vector, or `without` where there is none.
+__device__ __forceinline__ void nr_load8(float (&w)[8], const float* __restrict__ p, int c, float without) {
+  if (p == nullptr) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) w[k] = __ldg(p + k);
+    for (int k = 0; k < 8; ++k) w[k] = without;
+  } else if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {   // (the same for every piece of a vector)
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p + c)), b = __ldg(reinterpret_cast<const float4*>(p + c) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = __ldg(p + c + k);
+  }
 }
 
 // One row (LPR lanes of the warp; the others work on other rows): norm, rotation, store.
 // `on`: the row exists and is written; every lane takes part in the shuffles.
 template <int LPR, int STEPS, bool ALIGNED>
-__device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS][8], int lane_in, int part, int h,
-                                       int64_t orow, bool on, const float (&rc)[8], const float (&rsn)[8],
-                                       int rope_step, float* strip, const float* s_cos, const float* s_sin) {
-  const NormRows& R = P.part[part];
+__device__ __forceinline__ void nr_row(const NormRopeParams& P, const NormRows& R, float (&x)[STEPS][8], int lane_in,
+                                       int64_t at, bool on, const float (&wr)[8], const float (&br)[8],
+                                       const float (&rc)[8], const float (&rsn)[8], int rope_step, float* strip,
+                                       const float* s_cos, const float* s_sin) {
   const int pieces = P.d >> 3;
   const int np = P.norm_dim >> 3;                     // norm_dim is a multiple of 8: whole pieces
   const int half = P.rope >> 1;
-  if (P.part[0].norm | P.part[1].norm) {
-    const bool norm = R.norm != NORM_NONE;
-    const float inv_n = 1.f / static_cast<float>(P.norm_dim > 0 ? P.norm_dim : 1);
-    float mu = 0.f;
-    if (P.part[0].norm == NORM_LAYER || P.part[1].norm == NORM_LAYER) {
+  if (R.norm != NORM_NONE) {                          // (the same for all rows of an operand)
+    const float inv_n = 1.f / static_cast<float>(P.norm_dim);
+    if (R.norm == NORM_LAYER) {
       float a = 0.f;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
@@ -98,37 +109,36 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
 #pragma unroll
           for (int k = 0; k < 8; ++k) a += x[s][k];
         }
-      a = nr_row_sum<LPR>(a) * inv_n;
-      if (R.norm == NORM_LAYER) mu = a;
+      const float mu = nr_row_sum<LPR>(a) * inv_n;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+        if (LPR * s + lane_in < np) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[s][k] -= mu;
+        }
     }
     float q = 0.f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
       if (LPR * s + lane_in < np) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[s][k] -= mu;
-          q = fmaf(x[s][k], x[s][k], q);
-        }
+        for (int k = 0; k < 8; ++k) q = fmaf(x[s][k], x[s][k], q);
       }
-    q = nr_row_sum<LPR>(q);
-    if (norm) {
-      const float rs = 1.f / sqrtf(q * inv_n + P.eps);
+    const float rs = rsqrtf(nr_row_sum<LPR>(q) * inv_n + P.eps);
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const int c = LPR * s + lane_in;
-        if (c < np) {
+    for (int s = 0; s < STEPS; ++s) {
+      const int c = LPR * s + lane_in;
+      if (c < np) {
+        if (STEPS == 1) {                             // the lane's weights are in registers
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[s][k] = fmaf(x[s][k] * rs, wr[k], br[k]);
+        } else {
           float w[8];
-          if (R.weight) {
-            nr_load8(w, R.weight + 8 * c);
+          nr_load8(w, R.weight, 8 * c, 1.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[s][k] *= rs * w[k];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[s][k] *= rs;
-          }
+          for (int k = 0; k < 8; ++k) x[s][k] *= rs * w[k];
           if (R.bias) {
-            nr_load8(w, R.bias + 8 * c);
+            nr_load8(w, R.bias, 8 * c, 0.f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[s][k] += w[k];
           }
@@ -149,8 +159,8 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
           for (int k = 0; k < 8; k += 2) {
             const float a = x[s][k], b = x[s][k + 1];
             if (rotated) {
-              x[s][k] = fmaf(a, rc[k], -(b * rsn[k]));
-              x[s][k + 1] = fmaf(b, rc[k], a * rsn[k]);
+              x[s][k] = fmaf(a, rc[k], b * rsn[k]);
+              x[s][k + 1] = fmaf(b, rc[k + 1], a * rsn[k + 1]);
             }
           }
         } else {
@@ -160,8 +170,7 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float other = __shfl_sync(0xffffffffu, x[s][k], partner, LPR);
-            if (rotated)
-              x[s][k] = second ? fmaf(x[s][k], rc[k], other * rsn[k]) : fmaf(x[s][k], rc[k], -(other * rsn[k]));
+            if (rotated) x[s][k] = fmaf(x[s][k], rc[k], other * rsn[k]);
           }
         }
       }
@@ -195,7 +204,6 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
     }
     __syncwarp();
   }
-  const int64_t at = orow * R.heads + h;
   if (P.fp8) {
     float top = 0.f;
 #pragma unroll
@@ -203,8 +211,9 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[s][k]));
     top = nr_row_max<LPR>(top);
-    const float sc = top > 0.f ? top / 448.f : 1.f;
-    const float inv = 1.f / sc;                       // the quotient to fp32 rounding, far below an e4m3 step
+    // products with 1 / 448 and 1 / scale for the quotients: an ulp or two of fp32, far below an e4m3 step
+    const float sc = top > 0.f ? top * (1.f / 448.f) : 1.f;
+    const float inv = __frcp_rn(sc);
     if (on && lane_in == 0) R.scale[at] = sc;
     uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(R.out) + at * P.d);
 #pragma unroll
@@ -237,45 +246,99 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, float (&x)[STEPS
   }
 }
 
+// Heads h0 .. h1 of one operand of token t, by the block's warps from warp `w0` on.
 template <int LPR, int STEPS, bool ALIGNED>
-__global__ void __launch_bounds__(kNrWarps * 32)
-    norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
-  constexpr int kRows = 32 / LPR;                     // rows a warp works on at once
-  constexpr int kDeep = STEPS == 1 ? 2 : 1;           // and one after another, their loads issued together
-  __shared__ float s_cos[kNrMaxRope / 2], s_sin[kNrMaxRope / 2];
-  __shared__ float s_strip[ALIGNED ? 1 : kNrWarps * kRows][ALIGNED ? 1 : kNrMaxRope];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lane_in = lane % LPR, sub = lane / LPR;
-  const int t = blockIdx.x / P.blocks_per_token;
-  const int h0 = (blockIdx.x - t * P.blocks_per_token) * P.chunk;
-  const int pieces = P.d >> 3;
-  const int heads = P.part[0].heads + P.part[1].heads;
-  const int h_end = h0 + P.chunk < heads ? h0 + P.chunk : heads;
-  const int half = P.rope >> 1;
-
-  const int stride = kNrWarps * kRows;
+struct NrRows {
+  static constexpr int kWarps = nr_warps(STEPS);
+  static constexpr int kRows = 32 / LPR;              // rows a warp works on at once
+  static constexpr int kDeep = STEPS == 1 ? 2 : 1;    // and one after another, their loads issued together
+  static constexpr int kStride = kWarps * kRows;
   uint4 raw[kDeep][STEPS];
-  auto fetch = [&](int base) {
+
+  __device__ __forceinline__ void fetch(const NormRopeParams& P, const NormRows& R, const uint16_t* xt, int base,
+                                        int h1, int lane_in) {
+    const int pieces = P.d >> 3;
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int hh = base + u * stride;
-      const bool in = hh < h_end;
-      const int part = in && hh >= P.part[0].heads ? 1 : 0;
-      const NormRows& R = P.part[part];
-      const int h = part ? hh - P.part[0].heads : hh;
-      const uint4* src = reinterpret_cast<const uint4*>(R.x + t * R.x_stride + static_cast<int64_t>(h) * P.d);
+      const int h = base + u * kStride;
+      const uint4* src = reinterpret_cast<const uint4*>(xt + h * P.d);
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int c = LPR * s + lane_in;
-        raw[u][s] = in && c < pieces ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        raw[u][s] = h < h1 && c < pieces ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
-  };
-  const int first = h0 + warp * kRows + sub;
-  fetch(first);                                       // in flight while the angles are formed
+  }
+  __device__ __forceinline__ void run(const NormRopeParams& P, const NormRows& R, int t, int h0, int h1, int w0,
+                                      bool fetched, int warp, int lane, const float (&rc)[8], const float (&rsn)[8],
+                                      int rope_step, float* strip, const float* s_cos, const float* s_sin) {
+    const int lane_in = lane % LPR, sub = lane / LPR;
+    const uint16_t* xt = R.x + t * R.x_stride;
+    int64_t orow = t;
+    bool has = true;
+    if (R.slots) {
+      orow = __ldg(R.slots + t);
+      has = orow >= 0 && orow < R.out_rows;           // -1: the token has no row
+      if (!has) {
+        if (orow != -1 && threadIdx.x == 0 && h0 == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
+        return;
+      }
+    }
+    float wr[8], br[8];
+    if (STEPS == 1) {
+      const bool in = R.norm != NORM_NONE && lane_in < (P.norm_dim >> 3);
+      nr_load8(wr, in ? R.weight : nullptr, 8 * lane_in, 1.f);
+      nr_load8(br, in ? R.bias : nullptr, 8 * lane_in, 0.f);
+    }
+    const int64_t at0 = orow * R.heads;
+    const int first = h0 + ((warp + kWarps - w0) % kWarps) * kRows;
+    for (int base = first; base < h1; base += kDeep * kStride) {
+      if (!fetched || base != first) fetch(P, R, xt, base + sub, h1, lane_in);
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        if (base + u * kStride >= h1) break;          // (uniform over the warp)
+        const int h = base + sub + u * kStride;
+        const bool on = h < h1;
+        float x[STEPS][8];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const uint32_t w[4] = {raw[u][s].x, raw[u][s].y, raw[u][s].z, raw[u][s].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[s][2 * k] = __uint_as_float(w[k] << 16);
+            x[s][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+        nr_row<LPR, STEPS, ALIGNED>(P, R, x, lane_in, at0 + (on ? h : 0), on, wr, br, rc, rsn, rope_step, strip, s_cos,
+                                    s_sin);
+      }
+    }
+  }
+};
+
+template <int LPR, int STEPS, bool ALIGNED>
+__global__ void __launch_bounds__(nr_warps(STEPS) * 32)
+    norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
+  using Rows = NrRows<LPR, STEPS, ALIGNED>;
+  __shared__ float s_cos[kNrMaxRope / 2], s_sin[kNrMaxRope / 2];
+  __shared__ float s_strip[ALIGNED ? 1 : Rows::kWarps * Rows::kRows][ALIGNED ? 1 : kNrMaxRope];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane_in = lane % LPR, sub = lane / LPR;
+  const int t = blockIdx.x / P.blocks_per_token;
+  // the block's share of the token's rows, the queries' first
+  const int r0 = (blockIdx.x - t * P.blocks_per_token) * P.chunk, nq = P.part[0].heads;
+  const int r1 = r0 + P.chunk < nq + P.part[1].heads ? r0 + P.chunk : nq + P.part[1].heads;
+  const int q0 = r0 < nq ? r0 : nq, q1 = r1 < nq ? r1 : nq;
+  const int k0 = r0 > nq ? r0 - nq : 0, k1 = r1 > nq ? r1 - nq : 0;
+  const int half = P.rope >> 1;
+
+  Rows rows;
+  const bool early = q0 < q1;                         // the first queries' loads are in flight while the angles are formed
+  if (early)
+    rows.fetch(P, P.part[0], P.part[0].x + t * P.part[0].x_stride, q0 + warp * Rows::kRows + sub, q1, lane_in);
   if (half > 0) {
     const int64_t pos = __ldg(P.pos + t);
-    for (int i = threadIdx.x; i < half; i += kNrWarps * 32) {
+    for (int i = threadIdx.x; i < half; i += Rows::kWarps * 32) {
       // the angle in half turns, reduced to [-1, 1]
       const double half_turns =
           static_cast<double>(pos) * static_cast<double>(__ldg(P.inv_freq + i)) * 0.31830988618379067;
@@ -284,7 +347,7 @@ __global__ void __launch_bounds__(kNrWarps * 32)
     }
   }
   __syncthreads();
-  // the cosines and sines of this lane's piece of the rotated step (ALIGNED)
+  // the cosines and the signed sines of this lane's piece of the rotated step (ALIGNED)
   float rc[8], rsn[8];
   const int rope_step = ALIGNED ? (P.rope_off >> 3) / LPR : 0;
   if (ALIGNED) {
@@ -292,43 +355,19 @@ __global__ void __launch_bounds__(kNrWarps * 32)
     const bool in = j >= 0 && 8 * j < P.rope;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int pair = P.interleaved ? 4 * j + (k >> 1) : (8 * j + k) % (half > 0 ? half : 1);
-      rc[k] = in ? s_cos[in ? pair : 0] : 1.f;
-      rsn[k] = in ? s_sin[in ? pair : 0] : 0.f;
+      const int e = 8 * j + k;                        // element of the rotated part; the first of a pair subtracts
+      const bool second = P.interleaved ? (k & 1) : e >= half;
+      const int pair = P.interleaved ? e >> 1 : second ? e - half : e;
+      rc[k] = in ? s_cos[pair] : 1.f;
+      rsn[k] = in ? (second ? s_sin[pair] : -s_sin[pair]) : 0.f;
     }
   }
-  for (int base = first - sub; base < h_end; base += kDeep * stride) {
-    if (base != first - sub) fetch(base + sub);
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      const int hh = base + sub + u * stride;
-      if (base + u * stride >= h_end) break;          // (uniform over the warp)
-      const bool in = hh < h_end;
-      const int part = in && hh >= P.part[0].heads ? 1 : 0;
-      const int h = part ? hh - P.part[0].heads : hh;
-      int64_t orow = t;
-      bool on = in;
-      if (part && P.part[1].slots) orow = __ldg(P.part[1].slots + t);
-      if (!part && P.part[0].slots) orow = __ldg(P.part[0].slots + t);
-      if (in && P.part[part].slots && (orow < 0 || orow >= P.part[part].out_rows)) {   // -1: the token has no row
-        if (orow != -1 && lane_in == 0) atomicOr(&g_fault, FAULT_BAD_INDEX);
-        on = false;
-      }
-      if (!on) orow = 0;
-      float x[STEPS][8];
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        const uint32_t w[4] = {raw[u][s].x, raw[u][s].y, raw[u][s].z, raw[u][s].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[s][2 * k] = __uint_as_float(w[k] << 16);
-          x[s][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
-      }
-      nr_row<LPR, STEPS, ALIGNED>(P, x, lane_in, part, h, orow, on, rc, rsn, rope_step,
-                                  s_strip[ALIGNED ? 0 : warp * kRows + sub], s_cos, s_sin);
-    }
-  }
+  float* strip = s_strip[ALIGNED ? 0 : warp * Rows::kRows + sub];
+  if (early)
+    rows.run(P, P.part[0], t, q0, q1, 0, true, warp, lane, rc, rsn, rope_step, strip, s_cos, s_sin);
+  if (k0 < k1)                                        // the keys start at the warp that has the fewest queries
+    rows.run(P, P.part[1], t, k0, k1, ((q1 - q0 + Rows::kRows - 1) / Rows::kRows) % Rows::kWarps, false, warp, lane, rc, rsn,
+             rope_step, strip, s_cos, s_sin);
 }
 
 template <int LPR, int STEPS>
@@ -338,9 +377,9 @@ inline void nr_launch(const NormRopeParams& p, unsigned blocks, cudaStream_t st)
   const bool aligned = p.rope == 0 || (p.rope_off % 8 == 0 && p.rope % (p.interleaved ? 8 : 16) == 0 &&
                                        piece / LPR == last / LPR);
   if (aligned)
-    norm_rope_kernel<LPR, STEPS, true><<<blocks, kNrWarps * 32, 0, st>>>(p);
+    norm_rope_kernel<LPR, STEPS, true><<<blocks, nr_warps(STEPS) * 32, 0, st>>>(p);
   else
-    norm_rope_kernel<LPR, STEPS, false><<<blocks, kNrWarps * 32, 0, st>>>(p);
+    norm_rope_kernel<LPR, STEPS, false><<<blocks, nr_warps(STEPS) * 32, 0, st>>>(p);
 }
 
 cudaError_t launch_norm_rope(const NormRopeParams& p0, int num_sms, cudaStream_t st) {
@@ -349,7 +388,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p0, int num_sms, cudaStream_t
   if (p.T == 0 || heads == 0) return cudaSuccess;
   // a block takes all heads of a token unless the tokens alone would leave SMs without a block
   int split = 1;
-  while (static_cast<int64_t>(p.T) * split < 2 * num_sms && split * kNrWarps < heads) split *= 2;
+  while (static_cast<int64_t>(p.T) * split < 2 * num_sms && 4 * split < heads) split *= 2;
   p.chunk = (heads + split - 1) / split;
   p.blocks_per_token = (heads + p.chunk - 1) / p.chunk;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.T) * p.blocks_per_token);
