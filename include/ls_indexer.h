@@ -515,9 +515,10 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  * Faults: a q_start that is not ascending in [0, T], more than max_q tokens,
  * a negative kv_len or rows outside [0, n_rows) set LS_FAULT_BAD_INDEX; rows
  * outside the cache are not read and weigh nothing.
- * Workspace: ls_window_attention_workspace_size() bytes (0 when the query rows
- * alone fill the machine); calls that overlap on the GPU, replays of captured
- * ones among them, need workspaces of their own.
+ * Workspace: ls_window_attention_workspace_size() bytes: parts of the query rows
+ * whose work is spread over several CTAs (at most 39 MB; 0 when whole tiles of
+ * query rows fill the machine evenly); calls that overlap on the GPU, replays
+ * of captured ones among them, need workspaces of their own.
  */
 size_t ls_window_attention_workspace_size(int B, int T, int H, int max_q, int window, int align, int n_sink);
 ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
@@ -576,7 +577,7 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
  *   weight, bias [norm_dim] fp32 or NULL (ones, zeros), shared by the heads
  *   out  [..][heads][d] bf16 or, out_dtype LS_KEY_FP8_E4M3, e4m3 codes with
  *        scale [..][heads] fp32: scale = max |y| / 448 (1 for a row of
- *        zeros), code = y / scale rounded to nearest even
+ *        zeros), code = y / scale to the nearest (both to an ulp or two of fp32)
  *   slots [T] int64 or NULL: the output row of token t, for a cache of
  *        out_rows rows; -1 writes nothing.  Other rows are left as they are;
  *        a slot outside [-1, out_rows) writes nothing and sets

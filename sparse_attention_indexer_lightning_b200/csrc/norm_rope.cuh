@@ -32,10 +32,10 @@ namespace lsi {
 
 constexpr int kNrMaxDim = 1024;
 constexpr int kNrMaxRope = 256;
-// Warps of a block.  What a block does once (the angles, a lane's part of them and of the weights) is worth more rows
-// where rows are short: 4096 x 33 rows of 128 elements take 26 us with two warps, 33 with four; 2048 x 129 rows of 576
-// elements 117 and 111.
-constexpr int nr_warps(int steps) { return steps == 1 ? 2 : 4; }
+// Warps of a block: one for rows of one step (no warp waits while another forms the angles: 4096 x 33 rows of 128
+// elements take 21 us, 26 with two warps, 33 with four), four for longer rows (2048 x 129 rows of 576 elements: 111 us,
+// 117 with two).
+constexpr int nr_warps(int steps) { return steps == 1 ? 1 : 4; }
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
 struct NormRows {
@@ -386,14 +386,17 @@ cudaError_t launch_norm_rope(const NormRopeParams& p0, int num_sms, cudaStream_t
   NormRopeParams p = p0;
   const int heads = p.part[0].heads + p.part[1].heads;
   if (p.T == 0 || heads == 0) return cudaSuccess;
-  // a block takes all heads of a token unless the tokens alone would leave SMs without a block
+  const int pieces = p.d / 8;
+  // A block takes all heads of a token unless that leaves SMs short of blocks: of 16 one-warp blocks each (500 tokens x
+  // 33 rows of 128 elements: 6.3 us, 11.9 undivided), of two larger ones.
+  const bool one_step = pieces <= 16 || (pieces > 24 && pieces <= 32);
+  const int64_t want = static_cast<int64_t>(one_step ? 16 : 2) * num_sms;
   int split = 1;
-  while (static_cast<int64_t>(p.T) * split < 2 * num_sms && 4 * split < heads) split *= 2;
+  while (static_cast<int64_t>(p.T) * split < want && 4 * split < heads) split *= 2;
   p.chunk = (heads + split - 1) / split;
   p.blocks_per_token = (heads + p.chunk - 1) / p.chunk;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.T) * p.blocks_per_token);
   // lanes per row and pieces per lane: the fewest idle lanes for d / 8 pieces
-  const int pieces = p.d / 8;
   if (pieces <= 8) nr_launch<8, 1>(p, blocks, st);
   else if (pieces <= 16) nr_launch<16, 1>(p, blocks, st);
   else if (pieces <= 24) nr_launch<8, 3>(p, blocks, st);
