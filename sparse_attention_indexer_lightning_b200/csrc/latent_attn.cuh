@@ -897,7 +897,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         }
       }
       if (!whole) {
-        const bool bad = la_mask_row(va, static_cast<uint32_t>(vis)) | la_mask_row(vb, static_cast<uint32_t>(vis >> 32));
+        bool bad = la_mask_row(va, static_cast<uint32_t>(vis));
+        if (hs == kLaHalf) {
+          bad |= la_mask_row(vb, static_cast<uint32_t>(vis >> 32));
+        } else {                                      // few rows: 16 columns, all among the first
+#pragma unroll
+          for (int j = 0; j < 32; ++j) vb[j] = 0xff800000u;
+        }
         // A cache row that holds something not finite gives every query row of the pair a logit that is not
         // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
         // arrival (two warps that clear the same piece store the same bytes).
@@ -1013,16 +1019,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       uint8_t* stage = smem + kLaOffP + quad * 4096;
       uint8_t* mine = stage + lane * 128;
       // (rolled loops: this code runs once an item, and what it takes of the instruction cache the tiles' code misses)
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < 8; ++c) {
         uint32_t x[32];
         if (nt > 0) {
           tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x);
           tmem_wait_ld(x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = 0u;
         }
         const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+        // (a row that saw nothing: its weights were 0 and its values finite, so the accumulator is 0)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = empty ? 0u : __float_as_uint(__uint_as_float(x[k]) * inv);
+        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * inv);
         if (wide) {                                   // 32 columns are 128 bytes
 #pragma unroll
           for (int k = 0; k < 8; ++k)
