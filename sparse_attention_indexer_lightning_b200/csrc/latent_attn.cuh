@@ -561,7 +561,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   extern __shared__ __align__(1024) uint8_t la_raw[];
   uint8_t* smem = la_raw;
   if (smem_u32(smem) & 1023u) {                       // the swizzle needs what the declaration asks for
-    if (threadIdx.x == 0) atomicOr(&g_fault, FAULT_WAIT_TIMEOUT);
+    if (threadIdx.x == 0) {
+      atomicOr(&g_fault, FAULT_WAIT_TIMEOUT);
+      if (P.cut && (blockIdx.x & 1) == 0) P.joins[blockIdx.x >> 1] = LaJoin{0, 0, 0};
+    }
     return;
   }
   LaBars* bars = reinterpret_cast<LaBars*>(smem + kLaOffBars);

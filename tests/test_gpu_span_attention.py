@@ -172,6 +172,12 @@ def tree(L, d, branches, kind="random", window=0, align=1, n_sink=0, what="", dt
     return out, lse
 
 
+def tree_call(L, d, branches, **kw):
+    words = (max(d["ns"]) + 63) // 64
+    return L.ls_tree_attention(d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]),
+                               dev(tree_bits(branches, words)), row_off=dev(d["off"]), **kw)
+
+
 TREES = [
     # tokens, context, heads, window, align, sinks
     ([1], [0], 128, 0, 1, 0),
@@ -263,6 +269,44 @@ def test_rows_outside_the_sequences_are_left(L):
         out = torch.full((d["T"], 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
         window(L, d, kw["window"], 1, kw["n_sink"], out=out)
         assert torch.all(out[:3] == 7) and torch.all(out[-3:] == 7)
+
+
+def test_outputs_given_and_left(L):
+    """Cut work (one item over many pairs) and whole items: tokens outside the sequences keep what out held, lse is
+    optional, and max_q bounds what is computed."""
+    for lens, H in (([9000], 16), ([30], 128)):
+        d = make([3], lens, H, "marks", seed=21, drafted=True, pad=2)
+        branches = random_tree(d["rng"], d["ns"], pad=2)
+        want, _ = tree(L, d, branches, "marks")
+        out = torch.full((d["T"], H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        got, none = tree_call(L, d, branches, out=out, want_lse=False, max_q=3)
+        assert none is None and got is out and _same(got[2:5], want[2:5])
+        assert torch.all(out[:2] == 7) and torch.all(out[5:] == 7)
+    d = make([3], [700], 128, "marks", seed=22, pad=1)
+    out = torch.full((d["T"], 128, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    args = (d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]))
+    want, _ = L.ls_window_attention(*args, row_off=dev(d["off"]), window=600)
+    L.ls_window_attention(*args, row_off=dev(d["off"]), window=600, out=out, want_lse=False, max_q=3)
+    assert _same(out[1:4], want[1:4]) and torch.all(out[0] == 7) and torch.all(out[4] == 7)
+    assert L.ls_device_status() == 0
+
+
+def test_two_calls_at_once(L):
+    """Two calls on two streams, each with its workspace, beside one another, and sequences that share their rows."""
+    d = make([2, 2], [5000, 5000], 16, seed=23, drafted=True)
+    d["off"][1] = d["off"][0]                             # the second sequence reads the first one's rows
+    branches = [{0}, {0, 1}] * 2
+    want = tree(L, d, branches)
+    args = (d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]), dev(tree_bits(branches, 1)))
+    off = dev(d["off"])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(20):
+        outs.append(L.ls_tree_attention(*args, row_off=off, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for o, z in outs:
+        assert _same(o, want[0]) and _same(z, want[1])
 
 
 def test_splits_agree_and_repeat(L):

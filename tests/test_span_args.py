@@ -107,3 +107,19 @@ def test_norm_oracle_by_hand():
     assert np.allclose(y[0, 0, 4:], [-2, 1, 3, 4])
     y = oa.norm_rope(x, [1], [np.pi / 2, 0.0], "none", 8, None, None, 0.0, 4, False)
     assert np.allclose(y[0, 0, 4:], [-3, 2, 1, 4])
+
+
+def test_bindings_refuse_host_tensors():
+    import torch
+
+    import sparse_attention_indexer_lightning_b200 as ls
+    q = torch.zeros(2, 16, 576, dtype=torch.bfloat16)
+    lat, i32 = torch.zeros(9, 576, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: ls.ls_window_attention(q, lat, i32, i32[:1]),
+                 lambda: ls.ls_tree_attention(q, lat, i32, i32[:1], torch.zeros(2, 1, dtype=torch.int64)),
+                 lambda: ls.ls_norm_rope(q, None, torch.zeros(2, dtype=torch.int64), torch.ones(32)),
+                 lambda: ls.ls_norm_rope()):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        ls.ls_tree_attention(q, lat, i32, i32[:1], None)
