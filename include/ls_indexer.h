@@ -540,7 +540,8 @@ ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const i
  * being ctx_len[b] + (drafted rows that it sees) - 1 (at least ctx_len[b]);
  * drafted rows are never cut.  window = 0: the whole context.
  *
- *   tree_mask [T][words] 64-bit words, words >= ceil(max_q / 64)
+ *   tree_mask [T][words] 64-bit words, words >= 1; drafted rows past
+ *        64 * words have no bit and are not seen
  *   max_ctx: the longest context, as far as the caller knows it (0: unknown);
  *        it decides how the work is split, not what is computed, and the
  *        workspace query has to be given the same

@@ -1783,7 +1783,7 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
                "window >= 0, align >= 1, window + align <= 2^30)",
                B, T, H, max_q, window, align, n_sink);
   max_q = std::min(max_q, T);
-  LS_CHECK_ARG(words >= (max_q + 63) / 64, "tree_mask has %d words a token for max_q = %d", words, max_q);
+  LS_CHECK_ARG(words >= 1 && words <= (1 << 20), "tree_mask must have 1 to 2^20 words a token (got %d)", words);
   LS_CHECK_ARG(tree_mask || T == 0 || B == 0, "null tree_mask");
   LatentAttnParams p;
   p.q = q;

@@ -395,7 +395,7 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
   LaSpan& sp = w.sp;
   if (is_tree) {
     const int ctx = kv < avail ? kv : avail;
-    sp.drafted = avail - ctx;
+    sp.drafted = avail - ctx < 64 * P.words ? avail - ctx : 64 * P.words;   // rows past the mask's words are not seen
     sp.hi = sp.hi_min = ctx;
     sp.lo = la_window_lo(kv, P.window, P.align);      // a token's depth is 0 at least, n - 1 at most
     sp.lo_max = la_window_lo(kv + n - 1, P.window, P.align);

@@ -291,6 +291,17 @@ def test_outputs_given_and_left(L):
     assert L.ls_device_status() == 0
 
 
+def test_fewer_mask_words_than_drafted_rows(L):
+    """Drafted rows past the mask's words are not seen, and no word past a token's own is read (the last token's mask
+    ends with the tensor)."""
+    d = make([150], [90], 16, "marks", seed=24, drafted=True)
+    branches = [{i for i in range(150) if i % 3 == t % 3 and i <= t} for t in range(150)]
+    cut = [{i for i in b if i < 64} for b in branches]
+    tree(L, d, cut, "marks", words=1)
+    d = make([8] * 12, [100] * 12, 16, "marks", seed=25, drafted=True)   # one word does for all, whatever T is
+    tree(L, d, random_tree(d["rng"], d["ns"]), "marks", words=1)
+
+
 def test_two_calls_at_once(L):
     """Two calls on two streams, each with its workspace, beside one another, and sequences that share their rows."""
     d = make([2, 2], [5000, 5000], 16, seed=23, drafted=True)

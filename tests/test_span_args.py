@@ -41,7 +41,7 @@ def test_span_refusals(lib):
         assert window(lib, **kw) == 1, kw
     assert window(lib, d=512) == 3 and window(lib, dv=576) == 3
     assert window(lib, T=0) == 0 and window(lib, B=0) == 0 and window(lib, max_q=0) == 0
-    for kw in (dict(mask=None), dict(words=0), dict(T=130, max_q=129, words=2), dict(w=-1), dict(align=0),
+    for kw in (dict(mask=None), dict(words=0), dict(words=-1), dict(words=(1 << 20) + 1), dict(w=-1), dict(align=0),
                dict(n=0), dict(q=None)):
         assert tree(lib, **kw) == 1, kw
     assert tree(lib, d=128) == 3
