@@ -20,9 +20,13 @@
 // position of ten million an fp32 product is off by a radian; reduced to half
 // turns before the fp32 sine and cosine), and a lane keeps those of its pieces
 // in registers for all its rows.  Where the rotated part is whole pieces of
-// one step (kAligned), a rotation's partners are in the same piece
+// one step (ALIGNED), a rotation's partners are in the same piece
 // (interleaved) or in the same registers of another lane, one shuffle away;
 // any other offset goes through a strip of shared memory.
+//
+// Measured on a B200: 2048 x 129 rows of 576 elements 111 us, 5.5 TB/s (0.84 of
+// the measured copy); 4096 x 33 rows of 128 elements to fp8 21 us (2.5 TB/s:
+// 14 M warp instructions, the issue slots half used).
 
 #pragma once
 
