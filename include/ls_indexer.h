@@ -578,7 +578,8 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
  *   weight, bias [norm_dim] fp32 or NULL (ones, zeros), shared by the heads
  *   out  [..][heads][d] bf16 or, out_dtype LS_KEY_FP8_E4M3, e4m3 codes with
  *        scale [..][heads] fp32: scale = max |y| / 448 (1 for a row of
- *        zeros), code = y / scale to the nearest (both to an ulp or two of fp32)
+ *        zeros, 2^-149 at least for others), code = y / scale to the nearest
+ *        (both to an ulp or two of fp32)
  *   slots [T] int64 or NULL: the output row of token t, for a cache of
  *        out_rows rows; -1 writes nothing.  Other rows are left as they are;
  *        a slot outside [-1, out_rows) writes nothing and sets

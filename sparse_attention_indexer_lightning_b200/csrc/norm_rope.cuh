@@ -10,7 +10,7 @@
 //          (mu = 0 for the root-mean-square norm; y = x without a norm)
 //   (a, b) -> (a cos f - b sin f, b cos f + a sin f),  f = pos * inv_freq[i]
 //          for the pairs (2i, 2i + 1), interleaved, or (i, i + rope / 2)
-//   fp8: scale = max |y| / 448 (1 for a row of zeros), code = e4m3(y / scale)
+//   fp8: scale = max |y| / 448 (1 for a row of zeros, else 2^-149 at least), code = e4m3(y / scale)
 //
 // Bound by bytes: every element is read and written once; what has to stay
 // small beside them is the number of instructions per row.  LPR lanes (8, 16
@@ -25,7 +25,7 @@
 // any other offset goes through a strip of shared memory.
 //
 // Measured on a B200: 2048 x 129 rows of 576 elements 111 us, 5.5 TB/s (0.84 of
-// the measured copy); 4096 x 33 rows of 128 elements to fp8 21 us (2.5 TB/s:
+// the measured copy); 4096 x 33 rows of 128 elements to fp8 22 us (2.5 TB/s:
 // 14 M warp instructions, the issue slots half used).
 
 #pragma once
@@ -37,9 +37,10 @@ namespace lsi {
 constexpr int kNrMaxDim = 1024;
 constexpr int kNrMaxRope = 256;
 // Warps of a block: one for rows of one step (no warp waits while another forms the angles: 4096 x 33 rows of 128
-// elements take 21 us, 26 with two warps, 33 with four), four for longer rows (2048 x 129 rows of 576 elements: 111 us,
+// elements took 21 us, 26 with two warps, 33 with four), four for longer rows (2048 x 129 rows of 576 elements: 111 us,
 // 117 with two).
 constexpr int nr_warps(int steps) { return steps == 1 ? 1 : 4; }
+constexpr float kNrTinyScale = 0x1p-126f;   // the smallest normal number: reciprocals of scales from here on are finite
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
 struct NormRows {
@@ -215,9 +216,19 @@ __device__ __forceinline__ void nr_row(const NormRopeParams& P, const NormRows& 
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[s][k]));
     top = nr_row_max<LPR>(top);
-    // products with 1 / 448 and 1 / scale for the quotients: an ulp or two of fp32, far below an e4m3 step
-    const float sc = top > 0.f ? top * (1.f / 448.f) : 1.f;
-    const float inv = __frcp_rn(sc);
+    // Products with 1 / 448 and 1 / scale for the quotients: an ulp or two of fp32, far below an e4m3 step.  The
+    // reciprocal of a scale below kNrTinyScale may leave fp32 (and a zero's code would be 0 * inf): such a row's quotients
+    // are formed of 2^64 times both.
+    const float sc = top > 0.f ? fmaxf(top * (1.f / 448.f), 0x1p-149f) : 1.f;
+    const float up = sc < kNrTinyScale ? 0x1p64f : 1.f;
+    const float inv = __frcp_rn(sc * up);
+    // (a warp's vote: a division in a branch of each lane's own took 34 us for 4096 x 33 rows of 128 elements, this 22)
+    if (__any_sync(0xffffffffu, sc < kNrTinyScale)) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[s][k] *= up;
+    }
     if (on && lane_in == 0) R.scale[at] = sc;
     uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(R.out) + at * P.d);
 #pragma unroll
