@@ -499,9 +499,9 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  *
  *   q [T][H][576] bf16, latent [n_rows][576] bf16 (16-byte aligned)
  *   q_start [B+1] int32 ascending, kv_len [B] int32, row_off [B] int64 or NULL
- *   (zeros); H in [1, 1024]; T * H < 2^31
+ *   (zeros); B <= 2^24; H in [1, 1024]; T * H < 2^31
  *   max_q: at least the longest sequence's query tokens (T is always enough;
- *        the grid covers B * max_q tokens)
+ *        work is dealt out by the tokens that there are)
  *   out [T][H][512], fp32 or bf16 by out_dtype (LS_OUT_*); lse [T][H] fp32
  *        natural-log sum or NULL.  A token that sees no row gets out = 0 and
  *        lse = -inf.  Tokens before q_start[0] and from q_start[B] on are

@@ -12,6 +12,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -1643,6 +1644,13 @@ int query_tiles(int H, int max_q) {
   return static_cast<int>((static_cast<int64_t>(max_q) * H + kLaRows - 1) / kLaRows);
 }
 
+// Query tiles that hold query rows, at most: a sequence's last tile wastes 128 - gcd(H, 128) places at most, and a
+// call's sequences have T tokens between them (max_q alone, T by default, would count every sequence as the longest).
+int64_t span_items(int B, int T, int H, int max_q) {
+  const int64_t waste = static_cast<int64_t>(std::min(B, T)) * (kLaRows - std::gcd(H, kLaRows));
+  return std::min(static_cast<int64_t>(B) * query_tiles(H, max_q), (static_cast<int64_t>(T) * H + waste) / kLaRows);
+}
+
 size_t span_workspace(const LaLayout& l) {
   if (!l.cut) return 0;
   const size_t rows = 2 * static_cast<size_t>(l.pairs) * kLaRows;
@@ -1651,20 +1659,19 @@ size_t span_workspace(const LaLayout& l) {
 }
 
 bool span_sizes_ok(int B, int T, int H, int max_q, int window, int align, int n_sink, bool tree) {
-  return B >= 0 && T >= 0 && H >= 1 && H <= 1024 && max_q >= 0 && static_cast<int64_t>(T) * H <= 0x7fffffffLL &&
-         window >= (tree ? 0 : 1) && align >= 1 && n_sink >= 0 &&
+  // (B: a pair steps over 32 sequences in about a microsecond, and the others wait for its items)
+  return B >= 0 && B <= (1 << 24) && T >= 0 && H >= 1 && H <= 1024 && max_q >= 0 &&
+         static_cast<int64_t>(T) * H <= 0x7fffffffLL && window >= (tree ? 0 : 1) && align >= 1 && n_sink >= 0 &&
          static_cast<int64_t>(window) + align <= (1 << 30);
 }
 
-LaLayout window_layout(int B, int H, int max_q, int window, int align, int n_sink) {
-  return la_layout(static_cast<int64_t>(B) * query_tiles(H, max_q),
-                   span_tiles(H, max_q, 0, window, align, n_sink, 0));
+LaLayout window_layout(int B, int T, int H, int max_q, int window, int align, int n_sink) {
+  return la_layout(span_items(B, T, H, max_q), span_tiles(H, max_q, 0, window, align, n_sink, 0));
 }
 
-LaLayout tree_layout(int B, int H, int max_q, int64_t n_rows, int max_ctx, int window, int align, int n_sink) {
+LaLayout tree_layout(int B, int T, int H, int max_q, int64_t n_rows, int max_ctx, int window, int align, int n_sink) {
   const int64_t ctx = max_ctx > 0 && max_ctx < n_rows ? max_ctx : n_rows;
-  return la_layout(static_cast<int64_t>(B) * query_tiles(H, max_q),
-                   span_tiles(H, max_q, ctx, window, align, n_sink, max_q));
+  return la_layout(span_items(B, T, H, max_q), span_tiles(H, max_q, ctx, window, align, n_sink, max_q));
 }
 
 // 3-D bf16 map over rows of 576 elements as [panel of 64][row][64 elements], box = 64 x box_rows x box_panels,
@@ -1697,7 +1704,7 @@ ls_status span_attention(LatentAttnParams p, const LaLayout& lay, int d, int d_v
   LS_CHECK_ARG(p.q && latent && p.q_start && p.kv_len && p.out, "null tensor pointer");
   LS_CHECK_ARG(aligned16(p.q) && aligned16(latent) && aligned16(p.out), "q, latent and out must be 16-byte aligned");
   p.max_tiles = query_tiles(p.H, max_q);
-  LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles <= (1 << 30), "B * max_q * H too large");
+  LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles <= (1ll << 40), "B * max_q * H too large");
   p.pairs = lay.pairs;
   p.cut = lay.cut;
   p.out_bf16 = out_dtype == LS_OUT_BF16;
@@ -1734,7 +1741,7 @@ ls_status span_attention(LatentAttnParams p, const LaLayout& lay, int d, int d_v
 
 size_t ls_window_attention_workspace_size(int B, int T, int H, int max_q, int window, int align, int n_sink) {
   if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, false) || B == 0 || T == 0 || max_q == 0) return 0;
-  return span_workspace(window_layout(B, H, std::min(max_q, T), window, align, n_sink));
+  return span_workspace(window_layout(B, T, H, std::min(max_q, T), window, align, n_sink));
 }
 
 ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
@@ -1742,8 +1749,8 @@ ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const i
                               int64_t n_rows, int max_q, int window, int align, int n_sink, float scale,
                               int out_dtype, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   LS_CHECK_ARG(span_sizes_ok(B, T, H, max_q, window, align, n_sink, false),
-               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: H in [1, 1024], T * H < 2^31, "
-               "window and align >= 1, window + align <= 2^30)",
+               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: B <= 2^24, H in [1, 1024], "
+               "T * H < 2^31, window and align >= 1, window + align <= 2^30)",
                B, T, H, max_q, window, align, n_sink);
   max_q = std::min(max_q, T);
   LatentAttnParams p;
@@ -1762,7 +1769,7 @@ ls_status ls_window_attention(const uint16_t* q, const uint16_t* latent, const i
   p.out = out;
   p.lse = lse;
   LaLayout lay{1, 0};
-  if (B > 0 && max_q > 0) lay = window_layout(B, H, max_q, window, align, n_sink);
+  if (B > 0 && max_q > 0) lay = window_layout(B, T, H, max_q, window, align, n_sink);
   return span_attention(p, lay, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
 }
 
@@ -1770,7 +1777,7 @@ size_t ls_tree_attention_workspace_size(int B, int T, int H, int max_q, int64_t 
                                         int align, int n_sink) {
   if (!span_sizes_ok(B, T, H, max_q, window, align, n_sink, true) || n_rows < 1 || B == 0 || T == 0 || max_q == 0)
     return 0;
-  return span_workspace(tree_layout(B, H, std::min(max_q, T), n_rows, max_ctx, window, align, n_sink));
+  return span_workspace(tree_layout(B, T, H, std::min(max_q, T), n_rows, max_ctx, window, align, n_sink));
 }
 
 ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int32_t* q_start,
@@ -1779,8 +1786,8 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
                             int align, int n_sink, float scale, int out_dtype, void* out, float* lse, void* ws,
                             size_t ws_bytes, void* stream) {
   LS_CHECK_ARG(span_sizes_ok(B, T, H, max_q, window, align, n_sink, true),
-               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: H in [1, 1024], T * H < 2^31, "
-               "window >= 0, align >= 1, window + align <= 2^30)",
+               "bad sizes (B=%d T=%d H=%d max_q=%d window=%d align=%d n_sink=%d: B <= 2^24, H in [1, 1024], "
+               "T * H < 2^31, window >= 0, align >= 1, window + align <= 2^30)",
                B, T, H, max_q, window, align, n_sink);
   max_q = std::min(max_q, T);
   LS_CHECK_ARG(words >= 1 && words <= (1 << 20), "tree_mask must have 1 to 2^20 words a token (got %d)", words);
@@ -1804,7 +1811,7 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
   p.lse = lse;
   LaLayout lay{1, 0};
   if (B > 0 && max_q > 0 && n_rows >= 1)
-    lay = tree_layout(B, H, max_q, n_rows, max_ctx, window, align, n_sink);
+    lay = tree_layout(B, T, H, max_q, n_rows, max_ctx, window, align, n_sink);
   return span_attention(p, lay, d, d_v, latent, max_q, out_dtype, ws, ws_bytes, S(stream));
 }
 

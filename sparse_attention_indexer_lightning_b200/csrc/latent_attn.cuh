@@ -153,8 +153,7 @@ struct LaBars {
   uint64_t drain[2];                 // all MMAs of an issuing warp are complete
   uint32_t tmem_base;
   int abort_flag;
-  int64_t run_pos, run_end, run_base, run_total;      // cut form: this pair's run, see LaIter
-  int run_seq;
+  int idle;                          // cut form: the pair has no places
   LaItem item[kLaItems];
 };
 constexpr size_t kLaOffK = size_t(kLaPanels) * kLaPanelBytes;               // behind the query rows
@@ -428,73 +427,102 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
   return true;
 }
 
-// The items of a pair, the same in every role.
+// The items of a pair, found by the whole warp that hands them out: every sequence has places, laid out one behind
+// another.  Lane i holds the places of sequence b0 + i, so that sequences without tokens (a padded batch has many) are
+// stepped over 32 at a time.
 //
-// Whole items: pair p takes the items p, p + pairs, ... of B * max_tiles.
+// Whole items: one place per item; pair p takes the places p, p + pairs, ...  (Of one sequence, or a few sequences of one
+// item at most, the places are counted without a look at the tables, and some may have no item.)
 //
-// Cut: every sequence's items weigh its last one's tiles and kLaItemCost; laid out in order their weights sum to
-// run_total, and pair p takes the places run_total * p / pairs .. run_total * (p + 1) / pairs.  Place x of an item is
-// its tile x - kLaItemCost (the first places are its own cost; tiles beyond the weight belong to the last place).
+// Cut: every sequence's items weigh its last one's tiles and kLaItemCost; of the sum of all, pair p takes the places
+// total * p / pairs .. total * (p + 1) / pairs.  Place x of an item is its tile x - kLaItemCost (the first places are its
+// own cost; tiles beyond the weight belong to the last place).
 struct LaIter {
-  uint32_t id, step, items;                 // whole items
-  int64_t pos, end, base;                   // cut: next place, end of the run, first place of sequence b
-  int b, n_items, weight;
-  bool any;
-  __device__ __forceinline__ LaIter(const LatentAttnParams& P, const LaBars* bars) {
-    id = blockIdx.x >> 1;
-    step = gridDim.x >> 1;
-    items = static_cast<uint32_t>(P.B) * P.max_tiles;   // below 2^30
-    any = false;
-    n_items = weight = 0;
-    if (P.cut) {
-      pos = bars->run_pos;
-      end = bars->run_end;
-      base = bars->run_base;
-      b = bars->run_seq;
-    } else {
-      pos = end = base = 0;
-      b = 0;
+  int lane, pairs;
+  int64_t pos, end, base;                   // next place, end of the pair's, first place of sequence b0
+  int64_t total;                            // cut: all places
+  int b0, weight;                           // first sequence of the group; places per item of this lane's
+  int64_t mine, upto, group;                // places of this lane's sequence, with those before it, of the group
+  int64_t item_end;                         // cut: one behind the item's last place
+  bool guess;                               // places counted without the tables
+  __device__ __forceinline__ void start(const LatentAttnParams& P, LaBars* bars, int lane_) {
+    lane = lane_;
+    pairs = static_cast<int>(gridDim.x >> 1);
+    const int64_t p = blockIdx.x >> 1;
+    guess = !P.cut && (P.B == 1 || (P.max_tiles == 1 && P.B <= 4 * pairs));
+    base = total = item_end = 0;
+    pos = p;
+    end = INT64_MAX;
+    for (b0 = 0;; b0 += 32) {
+      load(P);
+      total += group;
+      if (!P.cut || b0 + 32 >= P.B) break;
+    }
+    if (!P.cut) return;
+    pos = total * p / pairs;
+    end = total * (p + 1) / pairs;
+    if (lane == 0) bars->idle = pos == end;
+    if (b0 > 0) {                           // the first group again
+      b0 = -32;
+      group = 0;
     }
   }
-  __device__ __forceinline__ bool next(const LatentAttnParams& P, bool tell, LaItem& w) {
-    int all;
-    if (!P.cut) {
-      for (; id < items; id += step) {
-        const uint32_t max_tiles = P.max_tiles;
-        const int seq = static_cast<int>(id / max_tiles);
-        if (la_item(P, seq, static_cast<int>(id - seq * max_tiles), tell, w, all)) {
-          id += step;
-          return true;
-        }
+  __device__ __forceinline__ void load(const LatentAttnParams& P) {
+    const int b = b0 + lane;
+    mine = 0;
+    weight = 1;
+    if (b < P.B) {
+      LaItem w;
+      int all;
+      if (guess) {
+        mine = P.max_tiles;
+      } else if (la_item(P, b, -1, blockIdx.x == 0, w, all)) {
+        if (P.cut) weight = w.nt + kLaItemCost;
+        mine = static_cast<int64_t>(all) * weight;
       }
-      return false;
     }
-    if (pos >= end) return false;
-    while (!any || pos >= base + static_cast<int64_t>(n_items) * weight) {   // the sequence of the next place
-      if (any) {
-        base += static_cast<int64_t>(n_items) * weight;
-        ++b;
+    upto = mine;                            // with those before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    group = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  __device__ __forceinline__ bool next(const LatentAttnParams& P, LaItem& w) {
+    while (pos < end) {
+      while (pos >= base + group) {
+        base += group;
+        b0 += 32;
+        if (b0 >= P.B) return false;
+        load(P);
       }
-      if (b >= P.B) return false;
-      any = true;
-      const bool has = la_item(P, b, -1, false, w, all);
-      n_items = has ? all : 0;
-      weight = has ? w.nt + kLaItemCost : 0;
+      const int f = __ffs(__ballot_sync(0xffffffffu, pos - base < upto)) - 1;
+      const int64_t first = base + __shfl_sync(0xffffffffu, upto - mine, f);
+      const int64_t at = pos - first;
+      const int per = P.cut ? __shfl_sync(0xffffffffu, weight, f) : 1;
+      const int64_t q = P.cut ? at / per : at;
+      int all;
+      const bool has = la_item(P, b0 + f, static_cast<int>(q), guess && (blockIdx.x & 1) == 0, w, all);
+      if (!P.cut) {
+        pos += pairs;
+        if (has) return true;
+        continue;
+      }
+      item_end = first + (q + 1) * per;
+      const int x0 = static_cast<int>(at - q * per);
+      const int x1 = end - pos < per - x0 ? x0 + static_cast<int>(end - pos) : per;
+      const int n = w.nt;
+      int i0 = x0 - kLaItemCost, i1 = x1 - kLaItemCost;
+      i0 = i0 < 0 ? 0 : i0 < n ? i0 : n;
+      i1 = x1 == per ? n : i1 < 0 ? 0 : i1 < n ? i1 : n;
+      w.i0 = i0;
+      w.nt = i1 - i0;
+      if (x0 > 0 || x1 < per) w.part = 2 * static_cast<int>(blockIdx.x >> 1) + (x0 > 0 ? 0 : 1);
+      pos += x1 - x0;
+      return true;
     }
-    const int64_t at = pos - base;
-    const int64_t q = at / weight;
-    const int x0 = static_cast<int>(at - q * weight);
-    const int x1 = end - pos < weight - x0 ? x0 + static_cast<int>(end - pos) : weight;
-    la_item(P, b, static_cast<int>(q), false, w, all);
-    const int n = w.nt;
-    int i0 = x0 - kLaItemCost, i1 = x1 - kLaItemCost;
-    i0 = i0 < 0 ? 0 : i0 < n ? i0 : n;
-    i1 = x1 == weight ? n : i1 < 0 ? 0 : i1 < n ? i1 : n;
-    w.i0 = i0;
-    w.nt = i1 - i0;
-    if (x0 > 0 || x1 < weight) w.part = 2 * static_cast<int>(blockIdx.x >> 1) + (x0 > 0 ? 0 : 1);
-    pos += x1 - x0;
-    return true;
+    return false;
   }
 };
 
@@ -506,57 +534,6 @@ __device__ __forceinline__ bool la_next_item(LaBars* bars, int ic, LaItem& w, vo
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->item_empty[slot]);
   return true;
-}
-
-// The pair's run of the cut form (one warp of each CTA).
-__device__ __forceinline__ void la_plan(const LatentAttnParams& P, LaBars* bars, int lane) {
-  const int64_t p = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  int64_t total = 0, lo = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t before = 0;
-    bool found = false;
-    for (int b0 = 0; b0 < P.B && !found; b0 += 32) {
-      const int b = b0 + lane;
-      int64_t mine = 0;
-      if (b < P.B) {
-        LaItem w;
-        int all;
-        if (la_item(P, b, -1, pass == 0 && blockIdx.x == 0, w, all))
-          mine = static_cast<int64_t>(all) * (w.nt + kLaItemCost);
-      }
-      int64_t upto = mine;                            // with the sequences before it in this group of 32
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const int64_t group = __shfl_sync(0xffffffffu, upto, 31);
-      if (pass == 1) {
-        const uint32_t in = __ballot_sync(0xffffffffu, lo < before + upto);
-        if (in) {
-          found = true;
-          const int first = __ffs(in) - 1;
-          if (lane == first) {
-            bars->run_seq = b;
-            bars->run_base = before + upto - mine;
-          }
-        }
-      }
-      before += group;
-    }
-    if (pass == 0) {
-      total = before;
-      lo = total * p / pairs;
-      if (lane == 0) {
-        bars->run_total = total;
-        bars->run_pos = lo;
-        bars->run_end = total * (p + 1) / pairs;
-        bars->run_seq = P.B;                          // nothing to do unless the second pass finds the place
-        bars->run_base = 0;
-      }
-      __syncwarp();
-    }
-  }
 }
 
 // Persistent: the roles run through the pair's items (LaIter) at their own pace: the next item's query, first tiles and logits are on their way while the
@@ -615,11 +592,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
-  if (warp == 2 && P.cut) la_plan(P, bars, lane);
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&M.q);
-    tma_prefetch_desc(&M.k);
-    tma_prefetch_desc(&M.v);
+  LaIter it;
+  if (warp == 0) {
+    __syncwarp();
+    it.start(P, bars, lane);
+    if (lane == 0) {
+      tma_prefetch_desc(&M.q);
+      tma_prefetch_desc(&M.k);
+      tma_prefetch_desc(&M.v);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -628,53 +609,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ query and key copies
-    // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).
-    if (lane == 0) {
-      const bool first = cr == 0;
-      const uint32_t qfull = la_map(&bars->qfull, 0);
-      const uint32_t k_full[3] = {la_map(&bars->k_full[0], 0), la_map(&bars->k_full[1], 0), la_map(&bars->k_full[2], 0)};
-      bool ok = true;
-      int g = 0, qn = 0;
-      LaIter it(P, bars);
-      LaJoin join{0, 0, 0};
-      for (int ic = 0; ok; ++ic) {
-        LaItem w;
-        if (!it.next(P, first, w)) w.nt = -1;
+    // ------------------------------------------------------------ items, query and key copies
+    // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).  All lanes
+    // look for the next item, one hands it on and copies.
+    const bool first = cr == 0;
+    const uint32_t qfull = la_map(&bars->qfull, 0);
+    const uint32_t k_full[3] = {la_map(&bars->k_full[0], 0), la_map(&bars->k_full[1], 0), la_map(&bars->k_full[2], 0)};
+    int g = 0, qn = 0;
+    LaJoin join{0, 0, 0};
+    bool ok = true;
+    for (int ic = 0;; ++ic) {
+      LaItem w;
+      if (!it.next(P, w)) w.nt = w.part = -1;
+      if (lane == 0) {
         const int slot = ic % kLaItems;
-        if (!mbar_wait<false>(&bars->item_empty[slot], ((ic / kLaItems) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        bars->item[slot] = w;
-        mbar_arrive(&bars->item_full[slot]);
-        if (w.nt < 0) break;
-        if (w.part >= 0 && (w.part & 1)) {            // begins in this run and goes on in the next pairs'
-          const int64_t pairs = gridDim.x >> 1, item_end = it.base + ((it.pos - 1 - it.base) / it.weight + 1) * it.weight;
-          int64_t k = (blockIdx.x >> 1) + 1;
-          while (k < pairs && bars->run_total * k / pairs < item_end) ++k;
-          join.row0 = w.grow0;
-          join.nrows = w.nrows;
-          join.parts = static_cast<int>(k - (blockIdx.x >> 1));
-        }
-        if (w.nt == 0) continue;
-        if (!mbar_wait<false>(&bars->q_empty, (qn & 1) ^ 1, abort_flag)) { ok = false; break; }
-        ++qn;
-        if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
-        for (int c = 0; c < kLaKGroups; ++c)
-          la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, w.grow0 + kLaHalf * cr, kLaKPer * c);
-        for (int i = 0; i < w.nt && ok; ++i) {
-          int kind, a, cnt;
-          w.sp.tile(w.i0 + i, kind, a, cnt);
-          const int box = la_box_rows(cnt) / 2;       // this CTA's half of the rows
-          const int row = (kind ? w.rowd : w.row0) + a + box * cr;
-#pragma unroll
-          for (int c = 0; c < kLaKGroups; ++c) {
-            if (!mbar_wait<false>(&bars->k_empty[c], ((g + i) & 1) ^ 1, abort_flag)) { ok = false; break; }
-            if (first) mbar_arrive_expect_tx(&bars->k_full[c], 2 * kLaKPer * box * 128);
-            la_load_3d(smem + kLaOffK + c * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full[c], row,
-                       kLaKPer * c);
+        ok = mbar_wait<false>(&bars->item_empty[slot], ((ic / kLaItems) & 1) ^ 1, abort_flag);
+        if (ok) {
+          bars->item[slot] = w;
+          mbar_arrive(&bars->item_full[slot]);
+          if (w.part >= 0 && (w.part & 1)) {          // begins in this run and goes on in the next pairs'
+            int64_t k = (blockIdx.x >> 1) + 1;
+            while (k < it.pairs && it.total * k / it.pairs < it.item_end) ++k;
+            join.row0 = w.grow0;
+            join.nrows = w.nrows;
+            join.parts = static_cast<int>(k - (blockIdx.x >> 1));
           }
         }
-        g += w.nt;
+        if (ok && w.nt > 0) ok = mbar_wait<false>(&bars->q_empty, (qn & 1) ^ 1, abort_flag);
+        if (ok && w.nt > 0) {
+          ++qn;
+          if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
+          for (int c = 0; c < kLaKGroups; ++c)
+            la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, w.grow0 + kLaHalf * cr, kLaKPer * c);
+          for (int i = 0; i < w.nt && ok; ++i) {
+            int kind, a, cnt;
+            w.sp.tile(w.i0 + i, kind, a, cnt);
+            const int box = la_box_rows(cnt) / 2;     // this CTA's half of the rows
+            const int row = (kind ? w.rowd : w.row0) + a + box * cr;
+#pragma unroll
+            for (int c = 0; c < kLaKGroups; ++c) {
+              if (!mbar_wait<false>(&bars->k_empty[c], ((g + i) & 1) ^ 1, abort_flag)) { ok = false; break; }
+              if (first) mbar_arrive_expect_tx(&bars->k_full[c], 2 * kLaKPer * box * 128);
+              la_load_3d(smem + kLaOffK + c * kLaKPer * kLaPanelBytes, box == kLaHalf ? &M.k : &M.k_few, k_full[c], row,
+                         kLaKPer * c);
+            }
+          }
+          g += w.nt;
+        }
       }
+      if (w.nt < 0 || !__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+    }
+    if (lane == 0) {
       if (P.cut && first) P.joins[blockIdx.x >> 1] = join;
       if (!ok) la_settle();
     }
@@ -835,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     float* xch = reinterpret_cast<float*>(smem + kLaOffX);
     const uint32_t pfull0 = la_map(&bars->pfull, 0);
     // a pair without a run (fewer places than pairs) may lie between an item's parts: its own is empty
-    if (P.cut && cr == 0 && bars->run_pos == bars->run_end)
+    if (P.cut && cr == 0 && bars->idle)
       P.part_lse[2 * static_cast<int64_t>(blockIdx.x >> 1) * kLaRows + tl] = neg_inf();
     // logits in log2 units; a scale that is not above 0 turns (or clears) the logits first
     const bool turn = !(P.scale > 0.f);

@@ -1,0 +1,65 @@
+"""The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: batches whose max_q is left
+at its default.  Tolerances as in test_gpu_span_attention.py.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from parity_util import dev
+from test_gpu_span_attention import (  # noqa: F401
+    L, LOGIT, STEP, _same, check, make, random_tree, tree, tree_bits, tree_call, window,
+)
+
+pytestmark = pytest.mark.gpu
+
+
+def best_us(call, n=20, tries=4):
+    call()
+    best = 1e30
+    for _ in range(tries):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(n):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3 / n)
+    return best
+
+
+def test_decode_batches_without_max_q(L):  # noqa: F811
+    """148 single tokens: with max_q left out every pair has its two items, as with max_q = 1 (dealt by places of padded
+    sequences all 148 would fall to one pair).  The two calls do the same work, so 1.5 times is far from their noise."""
+    B = 148
+    lens = [int(x) for x in np.random.default_rng(34).integers(1, 900, B)]
+    d = make([1] * B, lens, 128, "random", seed=34)
+    window(L, d, 512, 1, 4)
+    window(L, d, 512, 1, 4, dtype=torch.float32, max_q=1)
+    args = (d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]))
+    call = lambda **kw: L.ls_window_attention(*args, row_off=dev_off, window=512, n_sink=4, **kw)  # noqa: E731
+    dev_off = dev(d["off"])
+    assert _same(call()[0], call(max_q=1)[0])
+    assert best_us(call) < 1.5 * best_us(lambda: call(max_q=1))
+
+
+@pytest.mark.parametrize("ns,H", [([0] * 70 + [1] + [0] * 40 + [3, 0, 0, 9] + [0] * 100 + [2], 128),
+                                  ([1, 0] * 90, 16), ([5] * 33, 130), ([0] * 65, 16), ([90, 1, 0, 2], 128)])
+def test_ragged_batches_without_max_q(L, ns, H):  # noqa: F811
+    """Sequences without tokens before, between and behind the others, more of them than are looked at together; whole
+    items and cut ones."""
+    lens = [int(x) for x in np.random.default_rng(len(ns)).integers(0, 300, len(ns))]
+    d = make(ns, lens, H, "marks", seed=len(ns), drafted=True)
+    branches = random_tree(d["rng"], ns)
+    if sum(ns):
+        tree(L, d, branches, "marks")                     # contexts as long as the cache, as far as the host knows: cut
+        tree(L, d, branches, "marks", max_ctx=1)          # whole
+        d = make(ns, [n + m for n, m in zip(ns, lens)], H, "marks", seed=len(ns))
+        window(L, d, 64, 1, 4, "marks")
+    else:
+        d = make(ns, lens, H, "marks", seed=len(ns), drafted=True, pad=2)
+        out = torch.full((4, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        L.ls_tree_attention(d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]),
+                            torch.zeros(4, 1, dtype=torch.int64, device="cuda"), row_off=dev(d["off"]), out=out)
+        assert torch.all(out == 7) and L.ls_device_status() == 0
