@@ -1626,7 +1626,7 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
 namespace {
 
 // Tiles of the cache that one tile of query rows can meet, at most (as far as the host knows).
-int64_t span_tiles(int H, int max_q, int64_t ctx, int window, int align, int n_sink, int drafted) {
+int64_t span_tiles(int H, int max_q, int64_t ctx, int window, int align, int n_sink, int64_t drafted) {
   int64_t span = ctx;                                 // the whole context
   int64_t sinks = 0;
   if (window > 0) {
@@ -1634,7 +1634,7 @@ int64_t span_tiles(int H, int max_q, int64_t ctx, int window, int align, int n_s
     const int64_t w = static_cast<int64_t>(window) + align - 1 + toks - 1;
     if (ctx <= 0 || w < ctx) {
       span = w;
-      sinks = (n_sink + kLaTile - 1) / kLaTile;
+      sinks = (static_cast<int64_t>(n_sink) + kLaTile - 1) / kLaTile;
     }
   }
   return sinks + (span + kLaTile - 1) / kLaTile + (drafted + kLaTile - 1) / kLaTile;

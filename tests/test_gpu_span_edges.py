@@ -1,5 +1,5 @@
-"""The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: batches whose max_q is left
-at its default.  Tolerances as in test_gpu_span_attention.py.
+"""The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: n_sink at the largest int,
+batches whose max_q is left at its default.  Tolerances as in test_gpu_span_attention.py.
 """
 
 import numpy as np
@@ -12,6 +12,12 @@ from test_gpu_span_attention import (  # noqa: F401
 )
 
 pytestmark = pytest.mark.gpu
+
+
+def test_all_sinks(L):  # noqa: F811
+    """n_sink at the largest int: every row is one."""
+    d = make([3], [300], 16, "marks", seed=33)
+    window(L, d, 1, 1, (1 << 31) - 1, "marks")
 
 
 def best_us(call, n=20, tries=4):

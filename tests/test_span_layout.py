@@ -25,3 +25,11 @@ def test_many_padded_sequences_are_taken(lib):  # noqa: F811
     assert tree(lib, B=B, T=T, H=128, max_q=T, n=1 << 20, max_ctx=100000) == 2
     assert window(lib, B=(1 << 24) + 1) == 1
     assert lib.ls_window_attention_workspace_size((1 << 24) + 1, 4, 16, 4, 64, 1, 4) == 0
+
+
+def test_sinks_up_to_the_largest_int(lib):  # noqa: F811
+    """n_sink may say "all": the number of its tiles is formed in 64 bits."""
+    big = (1 << 31) - 1
+    size = lambda n: lib.ls_window_attention_workspace_size(1, 3, 16, 3, 512, 1, n)  # noqa: E731
+    assert size(big) == size(big - 500) == size(1 << 24) > 0
+    assert window(lib, sink=big) == 2 and window(lib, sink=big - 500) == 2
