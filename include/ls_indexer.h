@@ -501,7 +501,8 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  *   q_start [B+1] int32 ascending, kv_len [B] int32, row_off [B] int64 or NULL
  *   (zeros); B <= 2^24; H in [1, 1024]; T * H < 2^31
  *   max_q: at least the longest sequence's query tokens (T is always enough;
- *        work is dealt out by the tokens that there are)
+ *        work is dealt out by the tokens that there are).  0, like B = 0 and
+ *        T = 0, launches nothing: no table is looked at
  *   out [T][H][512], fp32 or bf16 by out_dtype (LS_OUT_*); lse [T][H] fp32
  *        natural-log sum or NULL.  A token that sees no row gets out = 0 and
  *        lse = -inf.  Tokens before q_start[0] and from q_start[B] on are
@@ -512,9 +513,10 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  * Precision: logits, sums and lse in fp32; the weights enter the value
  * contraction rounded to bf16 (an output is within 2^-8 of the largest
  * visible value magnitude before its own rounding).
- * Faults: a q_start that is not ascending in [0, T], more than max_q tokens,
- * a negative kv_len or rows outside [0, n_rows) set LS_FAULT_BAD_INDEX; rows
- * outside the cache are not read and weigh nothing.
+ * Faults: a q_start that is not ascending in [0, T], a sequence of more than
+ * max_q tokens, a negative kv_len or rows outside [0, n_rows) set
+ * LS_FAULT_BAD_INDEX; tokens past max_q may be left as they are, rows outside
+ * the cache are not read and weigh nothing.
  * Workspace: ls_window_attention_workspace_size() bytes: parts of the query rows
  * whose work is spread over several CTAs (at most 39 MB; 0 when whole tiles of
  * query rows fill the machine evenly); calls that overlap on the GPU, replays

@@ -718,6 +718,9 @@ def _span_call(q, latent, q_start, lens, lens_name, row_off, tree_mask, window, 
         else:
             raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {out_dtype}")
         max_q = T if max_q is None else int(max_q)
+        if max_q == 0:
+            # 0 launches nothing in C, and a table that names tokens after all would not be found out
+            max_q, ws = min(T, 1), None
         if scale is None:
             scale = 1.0 / math.sqrt(d)
         if out is None:

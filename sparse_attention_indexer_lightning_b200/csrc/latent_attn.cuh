@@ -173,7 +173,7 @@ struct LatentAttnParams {
   const uint64_t* tree = nullptr;     // [T][words] or nullptr: the window form
   int words = 0;
   int B = 0, T = 0, H = 0;
-  int max_tiles = 0;                  // 128-row tiles per sequence that the grid covers
+  int max_q = 0, max_tiles = 0;       // tokens of a sequence at most, and their tiles of 128 rows
   int64_t n_rows = 0;
   int window = 0, align = 1, n_sink = 0;   // window <= 0 (tree only): the whole context
   float scale = 0.f;
@@ -375,8 +375,8 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
   }
   const int n = w.n = t1 - w.t0;
   const int64_t seq_rows = static_cast<int64_t>(n) * H;
-  if (seq_rows > static_cast<int64_t>(P.max_tiles) * kLaRows && tell)
-    atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: the rest is not computed
+  if (n > P.max_q && tell)
+    atomicOr(&g_fault, FAULT_BAD_INDEX);              // more tokens than max_q: those past max_tiles are not computed
   const int tiles = static_cast<int>((static_cast<uint32_t>(seq_rows) + kLaRows - 1) / kLaRows);   // T * H < 2^31
   all = tiles < P.max_tiles ? tiles : P.max_tiles;
   if (qtile < 0) qtile = all - 1;

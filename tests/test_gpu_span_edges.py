@@ -1,5 +1,5 @@
 """The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: n_sink at the largest int,
-batches whose max_q is left at its default.  Tolerances as in test_gpu_span_attention.py.
+batches whose max_q is left at its default, more tokens than max_q.  Tolerances as in test_gpu_span_attention.py.
 """
 
 import numpy as np
@@ -69,3 +69,26 @@ def test_ragged_batches_without_max_q(L, ns, H):  # noqa: F811
         L.ls_tree_attention(d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]),
                             torch.zeros(4, 1, dtype=torch.int64, device="cuda"), row_off=dev(d["off"]), out=out)
         assert torch.all(out == 7) and L.ls_device_status() == 0
+
+
+def test_more_tokens_than_max_q(L):  # noqa: F811
+    """A sequence with more tokens than max_q sets the fault, whatever room the last tile of query rows has left; max_q = 0
+    is right for a batch without tokens, and no other."""
+    d = make([3, 5], [40, 50], 16, "marks", seed=35, pad=1)
+    args = (d["q"].cuda(), d["lat"].cuda(), dev(d["start"]), dev(d["lens"]))
+
+    def status(call, *a, **kw):
+        r = call(*a, row_off=dev(d["off"]), **kw)
+        torch.cuda.synchronize()
+        return r, L.ls_device_status()
+
+    assert status(L.ls_window_attention, *args, max_q=5)[1] == 0
+    mask = torch.zeros(10, 1, dtype=torch.int64, device="cuda")
+    for m in (4, 3, 1, 0):
+        assert status(L.ls_window_attention, *args, max_q=m)[1] == 2, m
+        assert status(L.ls_tree_attention, *args[:3], dev(np.array([20, 20], np.int32)), mask, max_q=m)[1] == 2, m
+        long = dev(np.array([20, 20], np.int32))
+        assert status(L.ls_tree_attention, *args[:3], long, mask, max_q=m, max_ctx=1)[1] == 2, m
+    out = torch.full((10, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    none = (args[0], args[1], torch.full((3,), 4, dtype=torch.int32, device="cuda"), args[3])
+    assert status(L.ls_window_attention, *none, max_q=0, out=out)[1] == 0 and torch.all(out == 7)
