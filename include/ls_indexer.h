@@ -509,7 +509,9 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  *        left as they are.
  * A visible row weighs by its logit; a masked one weighs exactly 0 whatever
  * it holds (NaN and infinities included).  A visible logit that is NaN or
- * +inf makes its (token, head) row NaN, and no other.
+ * +inf makes its (token, head) row NaN, and no other.  One of -inf weighs 0
+ * and leaves lse; where its row's value is not finite, out is NaN in those
+ * columns at least.
  * Precision: logits, sums and lse in fp32; the weights enter the value
  * contraction rounded to bf16 (an output is within 2^-8 of the largest
  * visible value magnitude before its own rounding).

@@ -1703,6 +1703,7 @@ ls_status span_attention(LatentAttnParams p, const LaLayout& lay, int d, int d_v
   if (p.B == 0 || p.T == 0 || max_q == 0) return LS_OK;
   LS_CHECK_ARG(p.q && latent && p.q_start && p.kv_len && p.out, "null tensor pointer");
   LS_CHECK_ARG(aligned16(p.q) && aligned16(latent) && aligned16(p.out), "q, latent and out must be 16-byte aligned");
+  p.latent = latent;
   p.max_q = max_q;
   p.max_tiles = query_tiles(p.H, max_q);
   LS_CHECK_ARG(static_cast<int64_t>(p.B) * p.max_tiles <= (1ll << 40), "B * max_q * H too large");

@@ -51,7 +51,10 @@
 // sees whole is checked for logits that are not finite, and only then the
 // staged values are searched for elements that are not finite (a weight of 0
 // times one of them would be NaN) and cleared.  A visible row with a NaN or
-// +inf logit makes its own query row NaN, and no other.
+// +inf logit makes its own query row NaN, and no other.  A visible logit of
+// -inf weighs 0, and 0 times a value that is not finite is NaN: a whole tile's
+// MMA gives that in the value's column, and of a cleared tile the rows in
+// question are looked at in the cache and make the whole query row NaN.
 //
 // Query rows that would leave pairs idle (few of them over a long span, or
 // sequences of very different lengths): the tiles of all of them, laid out one
@@ -167,6 +170,7 @@ static_assert(sizeof(LaBars) <= 640, "barrier block");
 static_assert(kLaSmem <= 232448, "shared memory budget");
 struct LatentAttnParams {
   const uint16_t* q = nullptr;        // [T * H][576]
+  const uint16_t* latent = nullptr;   // [n_rows][576]
   const int32_t* q_start = nullptr;   // [B + 1]
   const int32_t* kv_len = nullptr;    // [B]: window: rows with the tokens' own; tree: context rows
   const int64_t* row_off = nullptr;   // [B] or nullptr (0)
@@ -302,6 +306,37 @@ __device__ __forceinline__ bool la_mask_row(uint32_t (&v)[32], uint32_t vis) {
     if (!(vis & (1u << j))) v[j] = 0xff800000u;
   }
   return top >= 0x7f800000u;
+}
+
+// Rare: whether a lane's query row sees (`vis`: cache row `row0` and the 63 behind it) a cache row with a logit of -inf
+// (`low`: its bits before the scale's sign) and a value that is not finite.  Called by a whole warp, whose logits are
+// still at `scol`: reading them again keeps 64 comparisons out of the tiles' code.
+__device__ __noinline__ bool la_low_rows(const uint16_t* latent, int64_t row0, uint32_t scol, uint64_t vis,
+                                         uint32_t low) {
+  bool odd = false;
+#pragma unroll 1
+  for (int h = 0; h < 64; h += 32) {
+    uint32_t v[32], mine = 0u;
+    tmem_ld_32x32_nowait(scol + h, v);
+    tmem_wait_ld(v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) mine |= v[j] == low ? 1u << j : 0u;
+    mine &= static_cast<uint32_t>(vis >> h);
+    for (uint32_t todo = __reduce_or_sync(0xffffffffu, mine); todo; todo &= todo - 1) {
+      const int j = __ffs(todo) - 1;
+      const uint4* row = reinterpret_cast<const uint4*>(latent + (row0 + h + j) * kAttnLatent);
+      bool bad = false;
+      for (int c = threadIdx.x & 31; c < kAttnValue / 8; c += 32) {
+        const uint4 x = __ldg(row + c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          bad |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+      }
+      if (__any_sync(0xffffffffu, bad)) odd |= (mine >> j) & 1u;
+    }
+  }
+  return odd;
 }
 
 // One row's largest logit of a tile in log2 units (masked places hold -inf).
@@ -880,9 +915,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       tmem_ld_32x32_nowait(scol + 32, vb);
       tmem_wait_ld(va);
       tmem_wait_ld(vb);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) la_arrive_at(s_read[st]);
+      if (whole) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) la_arrive_at(s_read[st]);
+      }
       if (turn) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -902,6 +939,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
         // arrival (two warps that clear the same piece store the same bytes).
         if (__any_sync(0xffffffffu, bad)) {
+          // a weight of 0 times a visible value that is not finite is NaN, as in a whole tile: here the row's divisor is
+          if (la_low_rows(P.latent, static_cast<int64_t>(kind ? w.rowd : w.row0) + a, scol, vis,
+                          P.scale < 0.f ? 0x7f800000u : 0xff800000u))
+            lt = __uint_as_float(0x7fffffffu);
           if ((i > 0 && !la_wait(&bars->odone, (g - 1) & 1, abort_flag)) ||
               !la_wait_read(&bars->v_seen, vn & 1, abort_flag)) {
             ok = false;
@@ -922,7 +963,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           }
         }
       }
-      if (!whole) ++vn;
+      if (!whole) {
+        ++vn;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) la_arrive_at(s_read[st]);
+      }
       // the row's maximum: this thread's half and, from the other warp of the pair, the other half
       float mt = la_row_max(va, vb, sl2);
       xch[128 * st + tl] = mt;
@@ -996,7 +1042,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       const bool parts = w.part >= 0;
       const int64_t part_row = static_cast<int64_t>(w.part) * kLaRows + rq;
       if (half == 0 && live) {
-        const float v = empty ? neg_inf() : (m + log2f(l)) * 0.6931471805599453f;
+        // (a part that saw nothing but such rows is not empty: the join has to read its NaN)
+        const float v = empty ? neg_inf() : parts && l == 0.f ? lt : (m + log2f(l)) * 0.6931471805599453f;
         if (parts)
           P.part_lse[part_row] = v;
         else if (P.lse)

@@ -1,5 +1,6 @@
 """The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: n_sink at the largest int,
-batches whose max_q is left at its default, more tokens than max_q.  Tolerances as in test_gpu_span_attention.py.
+batches whose max_q is left at its default, more tokens than max_q, logits that are not finite.  Tolerances as in
+test_gpu_span_attention.py.
 """
 
 import numpy as np
@@ -92,3 +93,80 @@ def test_more_tokens_than_max_q(L):  # noqa: F811
     out = torch.full((10, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
     none = (args[0], args[1], torch.full((3,), 4, dtype=torch.int32, device="cuda"), args[3])
     assert status(L.ls_window_attention, *none, max_q=0, out=out)[1] == 0 and torch.all(out == 7)
+
+
+# Visible rows that are not finite: a context of 300 rows, so that the bad row lies in a tile that every token
+# sees whole (5, 130) or in one with places behind the last row (290).
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("max_ctx", [1, 0])
+@pytest.mark.parametrize("bad_row", [5, 130, 290])
+def test_visible_infinities(L, bad_row, max_ctx, dtype):  # noqa: F811
+    """A visible row with an infinity or a NaN in a value column: the (token, head) row is NaN where its logit is NaN or
+    +inf; where it is -inf (a weight of 0) that column is, and lse stays; in a whole tile and in one with masks alike.
+    An infinity in a key-only element with a logit of -inf weighs 0."""
+    d = make([2], [300], 16, seed=36, drafted=True)
+    branches = [{0}, {0, 1}]
+    q = d["q"].double()
+    q[:, :, 17] = torch.tensor([1.0, -1.0] * 8)
+    q[:, :, 550] = torch.tensor([-1.0] * 12 + [1.0] * 4)
+    d["q"] = q.to(torch.bfloat16)
+    for value, odd in ((float("inf"), 0), (-float("inf"), 1), (float("nan"), None)):
+        lat = d["lat"].clone()
+        lat[bad_row, 17] = value
+        out, lse = tree_call(L, dict(d, lat=lat), branches, out_dtype=dtype, max_ctx=max_ctx)
+        nan = slice(None) if odd is None else slice(odd, None, 2)
+        assert torch.isnan(out[:, nan].float()).all() and torch.isnan(lse[:, nan]).all()
+        assert torch.isnan(out[:, :, 17].float()).all()
+        if odd is not None:                               # the same lse as without that row
+            low = slice(1 - odd, None, 2)
+            assert not torch.isnan(lse[:, low]).any()
+            without = lat.clone()
+            without[bad_row] = 0.0
+            without[bad_row, 17] = 2.0 ** 100 if odd == 0 else -2.0 ** 100
+            assert _same(lse[:, low].contiguous(),
+                         tree_call(L, dict(d, lat=without), branches, max_ctx=max_ctx)[1][:, low].contiguous())
+    lat = d["lat"].clone()
+    lat[bad_row, 550] = float("inf")
+    e = dict(d, lat=d["lat"].clone())
+    out, lse = tree_call(L, dict(d, lat=lat), branches, out_dtype=dtype, max_ctx=max_ctx)
+    assert torch.isnan(out[:, 12:].float()).all() and torch.isnan(lse[:, 12:]).all()
+    # heads 0 .. 11: the same as without that row, which a level of -2^100 in a key-only element takes away
+    e["lat"][bad_row, 550] = 2.0 ** 100
+    want, wl = tree_call(L, e, branches, out_dtype=dtype, max_ctx=max_ctx)
+    assert _same(out[:, :12].contiguous(), want[:, :12].contiguous())
+    assert _same(lse[:, :12].contiguous(), wl[:, :12].contiguous())
+    assert L.ls_device_status() == 0
+
+
+def test_infinities_that_a_neighbour_does_not_see(L):  # noqa: F811
+    """The first row of a window, seen by the tile's first token alone, with a logit of -inf: the column that is infinite
+    there is NaN in that token's rows and its lse is as without that row; the others are as they were; and so it is when
+    the token is alone in its batch."""
+    d = make([3], [700], 16, seed=37)
+    q = d["q"].double()
+    q[:, :, 17] = -1.0
+    d["q"] = q.to(torch.bfloat16)
+    first = 700 - 3 - 200 + 1
+    lat = d["lat"].clone()
+    lat[first, 17] = float("inf")
+    good, gl = window(L, d, 200, 1, 4)
+    args = (dev(d["start"]), dev(d["lens"]))
+    out, lse = L.ls_window_attention(d["q"].cuda(), lat.cuda(), *args, row_off=dev(d["off"]), window=200, n_sink=4)
+    assert _same(out[1:], good[1:]) and _same(lse[1:], gl[1:])
+    assert torch.isnan(out[0, :, 17].float()).all() and torch.isfinite(lse).all()
+    one = dev(np.array([0, 1], np.int32))
+    out, alone = L.ls_window_attention(d["q"][:1].cuda(), lat.cuda(), one, dev(np.array([698], np.int32)), window=200,
+                                       n_sink=4)
+    assert torch.isnan(out[0, :, 17].float()).all() and (alone[0] - lse[0]).abs().max() <= 2 * LOGIT
+
+
+@pytest.mark.parametrize("max_ctx", [1, 0])
+def test_logits_below_the_fp32_range(L, max_ctx):  # noqa: F811
+    """A logit that leaves fp32 downwards (finite elements) weighs 0, in a whole tile and in one with masks."""
+    d = make([2], [300], 16, "marks", seed=38, drafted=True)
+    lat, q = d["lat"].double(), d["q"].double()
+    lat[:, 560], q[:, :, 560] = 0.0, -2.0 ** 90
+    for r in (7, 140, 295):
+        lat[r, 560] = 2.0 ** 60
+    d["lat"], d["q"] = lat.to(torch.bfloat16), q.to(torch.bfloat16)
+    tree(L, d, [{0}, {1}], "marks", dtype=torch.float32, max_ctx=max_ctx)
