@@ -241,7 +241,7 @@ __device__ __forceinline__ bool la_wait_all(uint64_t* bar, uint32_t parity, vola
 }
 
 // Address of this CTA's shared-memory object in CTA `rank` of the cluster, and an arrival there.  What the arrival
-// tells of (copies that have landed, weights behind a proxy fence) is read by the tensor cores alone, so it takes no
+// tells of (logits that have been read, weights behind a proxy fence) concerns the tensor cores alone, so it takes no
 // release over the cluster: that, and an acquire fence at the other end, cost 1000 cycles each (10000 cycles a tile).
 __device__ __forceinline__ uint32_t la_map(const void* p, uint32_t rank) {
   uint32_t a;
@@ -250,6 +250,18 @@ __device__ __forceinline__ uint32_t la_map(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void la_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The arrival, and a test of a phase that is known to be complete, for what the other CTA's warps read themselves: ordered
+// over the cluster.
+__device__ __forceinline__ void la_arrive_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void la_acquire(uint64_t* bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(parity)
+      : "memory");
 }
 __device__ __forceinline__ void la_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -703,6 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     // (a warp of their own: their places become free at another pace than the keys')
     if (lane == 0) {
       const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
+      const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
       bool ok = true;
       int g = 0;
       for (int ic = 0; ok; ++ic) {
@@ -722,6 +735,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
             if (cr == 0) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
             la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
                        4 * c + 2 * cr);
+          }
+          if (cr == 0 && ok && !w.sp.whole(kind, a, cnt, P.n_sink)) {
+            // both CTAs' softmax warps may read and clear these values; the other CTA's copies report to this one
+            // (this warp waits for the values' MMAs anyway: the MMA warp's tiles took 1000 cycles longer with it)
+            for (int c = 0; c < 2 && ok; ++c) {
+              ok = mbar_wait<false>(&bars->v_full[c], g & 1, abort_flag);
+              la_acquire(&bars->v_full[c], g & 1);
+            }
+            la_arrive_release(seen0);
+            la_arrive_release(seen1);
           }
         }
       }
@@ -791,7 +814,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     const uint64_t pdesc = sw128_kmajor_desc(base + static_cast<uint32_t>(kLaOffP)),
                    vdesc = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaTile * 128),
                    vdesc_few = sw128_mnmajor_desc(base + static_cast<uint32_t>(kLaOffV), kLaFew * 128);
-    const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
     bool ok = true;
     int g = 0;
     for (int ic = 0; ok; ++ic) {
@@ -804,14 +826,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         w.sp.tile(w.i0 + i, kind, a, cnt);
         const bool full = __shfl_sync(0xffffffffu, la_box_rows(cnt), 0) == kLaTile;
         if (!la_wait_all(&bars->v_full[0], g & 1, abort_flag)) { ok = false; break; }
-        if (!w.sp.whole(kind, a, cnt, P.n_sink)) {
-          if (!la_wait_all(&bars->v_full[1], g & 1, abort_flag)) { ok = false; break; }
-          if (lane == 0) {
-            la_arrive_at(seen0);
-            la_arrive_at(seen1);
-          }
-          __syncwarp();
-        }
         if (!la_wait_all(&bars->pfull, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t acc0 = i ? 1u : 0u;
@@ -948,6 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
             ok = false;
             break;
           }
+          la_acquire(&bars->v_seen, vn & 1);
           for (int c = 0; c < 2; ++c) {
             uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + c * kLaVGroup);
             for (int e = lane; e < 2 * 8 * 2 * hs; e += 32) {

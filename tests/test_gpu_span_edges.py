@@ -170,3 +170,45 @@ def test_logits_below_the_fp32_range(L, max_ctx):  # noqa: F811
         lat[r, 560] = 2.0 ** 60
     d["lat"], d["q"] = lat.to(torch.bfloat16), q.to(torch.bfloat16)
     tree(L, d, [{0}, {1}], "marks", dtype=torch.float32, max_ctx=max_ctx)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_masked_rows_that_are_not_finite_every_time(L, whole):  # noqa: F811
+    """300 calls bit for bit those over clean rows, with NaN and infinities in every masked row, many tiles a pair and
+    staged values to clear in most of them, in both CTAs."""
+    n, H, m = (74, 128, 1500) if whole else (40, 16, 1500)
+    d = make([n], [m], H, seed=n)
+    kw = dict(window=300, n_sink=70, out_dtype=torch.float32)
+    assert (L.lib().ls_window_attention_workspace_size(1, n, H, n, 300, 1, 70) == 0) == whole
+    q, args = d["q"].cuda(), (dev(d["start"]), dev(d["lens"]))
+    want, wl = L.ls_window_attention(q, d["lat"].cuda(), *args, **kw)
+    lat = d["lat"].clone()
+    for i, r in enumerate([r for r in range(lat.shape[0]) if r >= m or 70 <= r < m - n - 300 + 1]):
+        lat[r] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    lat = lat.cuda()
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        o, z = L.ls_window_attention(q, lat, *args, **kw)
+        bad += (o.view(torch.int32) != want.view(torch.int32)).sum() + (z.view(torch.int32) != wl.view(torch.int32)).sum()
+    assert int(bad) == 0 and L.ls_device_status() == 0
+
+
+@pytest.mark.parametrize("max_ctx", [1, 0])
+def test_branches_that_are_not_finite_every_time(L, max_ctx):  # noqa: F811
+    """The same for drafted rows: every odd token's row is not finite and seen by odd tokens alone, over several tiles of
+    drafted rows."""
+    n, H = 300, 16
+    d = make([n], [200], H, seed=41, drafted=True)
+    branches = [{i for i in range(n) if i % 2 == t % 2 and i <= t} for t in range(n)]
+    mask, q, args = dev(tree_bits(branches, 5)), d["q"].cuda(), (dev(d["start"]), dev(d["lens"]))
+    call = lambda lat: L.ls_tree_attention(q, lat, *args, mask, out_dtype=torch.float32, max_ctx=max_ctx)  # noqa: E731
+    want, wl = call(d["lat"].cuda())
+    lat = d["lat"].clone()
+    for i in range(1, n, 2):
+        lat[200 + i, (7 * i) % 512] = (float("nan"), float("inf"), -float("inf"))[i // 2 % 3]
+    lat = lat.cuda()
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        o, z = call(lat)
+        bad += (o[::2] != want[::2]).sum() + (z[::2] != wl[::2]).sum()
+    assert int(bad) == 0 and L.ls_device_status() == 0
