@@ -494,8 +494,12 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  *   lo = max(0, p - window + 1) rounded down to a multiple of align.
  * align = 1 is the sliding window of `window` rows, the token's own row
  * included; window = 1 with align = the block length is the bucket search's
- * window (a token's own, not yet clustered block), so that the result joins
- * that of ls_sparse_attention over the long-range keys by ls_attention_merge.
+ * window (a token's own, not yet clustered block).  The read lists of
+ * ls_lsa_*_select hold the sinks and that window already, so that
+ * ls_sparse_attention over a whole list is the whole attention.  To join this
+ * call's result with that over the long-range keys alone (ls_attention_merge
+ * wants disjoint parts), first set the entries of a list that are below n_sink
+ * or at least pos - pos % align to -1.
  *
  *   q [T][H][576] bf16, latent [n_rows][576] bf16 (16-byte aligned)
  *   q_start [B+1] int32 ascending, kv_len [B] int32, row_off [B] int64 or NULL

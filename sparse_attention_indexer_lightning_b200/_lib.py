@@ -768,7 +768,8 @@ def ls_window_attention(q, latent, q_start, kv_len, row_off=None, window: int = 
     q [T,H,576] bf16, the tokens of sequence b at q_start[b] .. q_start[b+1]-1; latent [R,576] bf16; q_start [B+1]
     and kv_len [B] int32, row_off [B] int64 or None: the sequence's kv_len rows (its query tokens' own ones last)
     start at row row_off.  The token at position p sees row j <= p when j < n_sink or j >= lo, lo = max(0,
-    p - window + 1) rounded down to a multiple of align (window=1, align=512: the block window of the LSA search).
+    p - window + 1) rounded down to a multiple of align (window=1, align=512: the block window of the LSA search, whose
+    read lists hold these rows already: set them to -1 there before the two attentions are joined).
     max_q: at least the longest sequence's query tokens (default T) -> (out [T,H,512] of out_dtype, lse [T,H] f32 or
     None); out_dtype=torch.float32 is what ls_attention_merge joins with other parts."""
     return _span_call(q, latent, q_start, kv_len, "kv_len", row_off, None, window, align, n_sink, max_q, 0, scale,

@@ -1,16 +1,17 @@
 """The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: n_sink at the largest int,
-batches whose max_q is left at its default, more tokens than max_q, logits that are not finite.  Tolerances as in
-test_gpu_span_attention.py.
+batches whose max_q is left at its default, more tokens than max_q, logits that are not finite, the read lists of
+the LSA search.  Tolerances as in test_gpu_span_attention.py.
 """
 
 import numpy as np
 import pytest
 import torch
 
-from parity_util import dev
+from parity_util import dev, dev_bf16
 from test_gpu_span_attention import (  # noqa: F401
     L, LOGIT, STEP, _same, check, make, random_tree, tree, tree_bits, tree_call, window,
 )
+from workloads.synth import make_lsa
 
 pytestmark = pytest.mark.gpu
 
@@ -170,6 +171,32 @@ def test_logits_below_the_fp32_range(L, max_ctx):  # noqa: F811
         lat[r, 560] = 2.0 ** 60
     d["lat"], d["q"] = lat.to(torch.bfloat16), q.to(torch.bfloat16)
     tree(L, d, [{0}, {1}], "marks", dtype=torch.float32, max_ctx=max_ctx)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_read_lists_of_the_lsa_search(L, H):  # noqa: F811
+    """keys_out holds the sinks and the window in front of the long-range keys: the sparse attention over the whole list,
+    and the block window joined with the sparse attention over the list without its sinks and window, agree; the two
+    whole parts joined would count sinks and window twice."""
+    T, N, block, n_sink = 24, 2100, 512, 4
+    s = make_lsa(T, N, block_keys=block, seed=39, chunk=True)
+    pos = dev(s["q_pos"])
+    assert s["q_pos"].tolist() == list(range(N - T, N))
+    keys, n = L.ls_lsa_flat_select(dev_bf16(s["q_idx"]), pos, dev_bf16(s["centroids"]), dev(s["bucket_off"]),
+                                   dev(s["bucket_mem"]), block_keys=block, n_sink=n_sink, top_p=64, budget=200)
+    d = make([T], [N], H, seed=39)
+    q, lat = d["q"].cuda(), d["lat"].cuda()
+    whole, wl = L.ls_sparse_attention(q, lat, keys, cuda_cores=True)
+    lo = (pos // block * block)[:, None]
+    far = torch.where((keys < n_sink) | (keys >= lo), torch.full_like(keys, -1), keys)
+    assert torch.equal((far >= 0).sum(1), n - n_sink - (pos - lo[:, 0] + 1)) and int((far >= 0).sum()) == 200 * T
+    near, nl = L.ls_window_attention(q, lat, dev(d["start"]), dev(d["lens"]), window=1, align=block, n_sink=n_sink,
+                                     out_dtype=torch.float32)
+    fo, fl = L.ls_sparse_attention(q, lat, far, cuda_cores=True)
+    o, z = L.ls_attention_merge(torch.stack([near, fo]), torch.stack([nl, fl]))
+    assert (z - wl).abs().max() <= 2 * LOGIT
+    assert (o - whole).abs().max() <= (STEP / (1 - STEP) + 5 * LOGIT) * lat.abs().max()
+    assert L.ls_device_status() == 0
 
 
 @pytest.mark.parametrize("whole", [True, False])
