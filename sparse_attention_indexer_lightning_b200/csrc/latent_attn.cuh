@@ -84,7 +84,8 @@ constexpr int kLaPanels = kAttnLatent / 64;           // 9 panels of 64 elements
 constexpr int kLaKGroups = 3, kLaKPer = 3;            // the key panels' groups
 constexpr int kLaPanelBytes = kLaHalf * 128;          // 8 KB: 64 elements of 64 rows
 constexpr int kLaVGroup = 2 * kLaTile * 128;          // 32 KB: two value panels of 128 rows
-constexpr int kLaThreads = 8 * 32;   // query and key copies, logit MMAs, output MMAs, 4 softmax / epilogue, value copies
+// items and query and key copies, logit MMAs, output MMAs, 4 softmax and epilogue, value copies
+constexpr int kLaThreads = 8 * 32;
 constexpr int kLaColO = 0, kLaColS = 256;             // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
 constexpr int kLaItemCost = 2;                        // an item's own cost in tiles: its query, its output
@@ -251,8 +252,8 @@ __device__ __forceinline__ uint32_t la_map(const void* p, uint32_t rank) {
 __device__ __forceinline__ void la_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The arrival, and a test of a phase that is known to be complete, for what the other CTA's warps read themselves: ordered
-// over the cluster.
+// The arrival, and a test of a phase that is known to be complete, for what the other CTA's warps read themselves:
+// ordered over the cluster.
 __device__ __forceinline__ void la_arrive_release(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -432,7 +433,8 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
   w.nrows = static_cast<int>(seq_rows - w.r0 < kLaRows ? seq_rows - w.r0 : kLaRows);
   w.grow0 = w.t0 * H + w.r0;
   const uint32_t first_row = static_cast<uint32_t>(w.r0);        // T * H < 2^31
-  const int tok_first = first_row / static_cast<uint32_t>(H), tok_last = (first_row + w.nrows - 1) / static_cast<uint32_t>(H);
+  const int tok_first = first_row / static_cast<uint32_t>(H);
+  const int tok_last = (first_row + w.nrows - 1) / static_cast<uint32_t>(H);
   const bool is_tree = P.tree != nullptr;
   const int own = is_tree ? n : 0;                    // drafted rows behind kv
   if ((kv < 0 || off < 0 || off > P.n_rows || kv + static_cast<int64_t>(own) > P.n_rows - off) && tell)
@@ -478,12 +480,12 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
 // another.  Lane i holds the places of sequence b0 + i, so that sequences without tokens (a padded batch has many) are
 // stepped over 32 at a time.
 //
-// Whole items: one place per item; pair p takes the places p, p + pairs, ...  (Of one sequence, or a few sequences of one
-// item at most, the places are counted without a look at the tables, and some may have no item.)
+// Whole items: one place per item; pair p takes the places p, p + pairs, ...  (Of one sequence, or a few sequences of
+// one item at most, the places are counted without a look at the tables, and some may have no item.)
 //
 // Cut: every sequence's items weigh its last one's tiles and kLaItemCost; of the sum of all, pair p takes the places
-// total * p / pairs .. total * (p + 1) / pairs.  Place x of an item is its tile x - kLaItemCost (the first places are its
-// own cost; tiles beyond the weight belong to the last place).
+// total * p / pairs .. total * (p + 1) / pairs.  Place x of an item is its tile x - kLaItemCost (the first places are
+// its own cost; tiles beyond the weight belong to the last place).
 struct LaIter {
   int lane, pairs;
   int64_t pos, end, base;                   // next place, end of the pair's, first place of sequence b0
@@ -583,9 +585,13 @@ __device__ __forceinline__ bool la_next_item(LaBars* bars, int ic, LaItem& w, vo
   return true;
 }
 
-// Persistent: the roles run through the pair's items (LaIter) at their own pace: the next item's query, first tiles and logits are on their way while the
-// output of the last one leaves.  Barrier phases follow counts that run on over the items: tiles (g), items with
-// tiles (qn), exchanges (xn).
+// Persistent: the roles run through the pair's items (LaIter) at their own pace: the next item's query, first tiles and
+// logits are on their way while the output of the last one leaves.  Barrier phases follow counts that run on over the
+// items: tiles (g), items with tiles (qn), exchanges (xn).
+//
+// The order of the roles in the source, and which branches are named rare, change where the tiles' loops lie in the code
+// and nothing else, but over 12 orders 16 tokens x 128 heads over 32768 rows took 132 to 164 us and 4096 tokens over a
+// window of 512 rows 763 to 821.  This order had the lowest mean over the cases.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
   extern __shared__ __align__(1024) uint8_t la_raw[];
@@ -655,7 +661,265 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
 
-  if (warp == 0) {
+  if (warp >= 3 && warp <= 6) {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int quad = warp & 3;                        // warps 3-6: tensor-memory lanes 32 * (warp & 3) ..
+    const int tl = quad * 32 + lane;                  // tensor-memory lane
+    const int r = tl & 63, half = tl >> 6;            // row of this CTA, and which half of a tile's rows
+    const int grp = quad & 1;                         // the two warps that share 32 rows
+    const int rq = kLaHalf * cr + r;                  // row of the pair
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* xch = reinterpret_cast<float*>(smem + kLaOffX);
+    const uint32_t pfull0 = la_map(&bars->pfull, 0);
+    // a pair without a run (fewer places than pairs) may lie between an item's parts: its own is empty
+    if (P.cut && cr == 0 && bars->idle)
+      P.part_lse[2 * static_cast<int64_t>(blockIdx.x >> 1) * kLaRows + tl] = neg_inf();
+    // logits in log2 units; a scale that is not above 0 turns (or clears) the logits first
+    const bool turn = !(P.scale > 0.f);
+    const float mult = P.scale < 0.f ? -1.f : 0.f;
+    const float sl2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
+    bool ok = true;
+    const uint32_t s_read[2] = {la_map(&bars->s_empty[0], 0), la_map(&bars->s_empty[1], 0)};
+    float* xsum = reinterpret_cast<float*>(smem + kLaOffL);
+    int g = 0, xn = 0, vn = 0;                        // tiles, exchanges, tiles that are not whole
+    for (int ic = 0; ok; ++ic) {
+      LaItem w;
+      if (!la_next_item(bars, ic, w, abort_flag)) { ok = false; break; }
+      const LaSpan& sp = w.sp;
+      const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
+      if (nt < 0) break;
+      const bool live = rq < w.nrows;
+      const int tok = (static_cast<uint32_t>(w.r0) + (live ? rq : w.nrows - 1)) / static_cast<uint32_t>(H);
+      // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
+      int hi, lo;
+      const uint64_t* branch = nullptr;
+      if (is_tree) {
+        branch = P.tree + static_cast<int64_t>(w.t0 + tok) * P.words;
+        int depth = 0;
+        if (P.window > 0) {
+          for (int c = 0; c < P.words; ++c) depth += __popcll(__ldg(branch + c) & la_low_mask(w.n - 64 * c));
+          depth = depth > 0 ? depth - 1 : 0;
+        }
+        hi = sp.hi;
+        lo = la_window_lo(w.kv + depth, P.window, P.align);
+      } else {
+        const int p = w.kv - w.n + tok;
+        hi = p + 1 < w.avail ? p + 1 : w.avail;
+        lo = la_window_lo(p, P.window, P.align);
+      }
+      float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
+      for (int i = 0; i < nt && ok; ++i, ++g) {
+        const int st = g & 1;
+        int kind, a0, cnt0;
+        sp.tile(w.i0 + i, kind, a0, cnt0);
+        const bool whole = sp.whole(kind, a0, cnt0, P.n_sink);
+        // this thread's rows of the tile: `hs` from a on, cnt of them in the tile
+        const int hs = la_box_rows(cnt0) / 2;
+        const int a = a0 + hs * half;
+        const int left = cnt0 - hs * half, cnt = left < 0 ? 0 : left < hs ? left : hs;
+        uint64_t vis = ~0ull;
+        if (!whole) {
+          if (kind == 0)
+            vis = la_low_mask(hi - a < cnt ? hi - a : cnt) & (la_low_mask(P.n_sink - a) | ~la_low_mask(lo - a));
+          else
+            vis = cnt > 0 ? (__ldg(branch + (a >> 6)) >> (a & 63)) & la_low_mask(cnt) : 0ull;
+        }
+        if (!la_wait(&bars->sfull[st], (g >> 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t va[32], vb[32];
+        const uint32_t scol = trow + kLaColS + 64 * st;
+        tmem_ld_32x32_nowait(scol, va);
+        tmem_ld_32x32_nowait(scol + 32, vb);
+        tmem_wait_ld(va);
+        tmem_wait_ld(vb);
+        if (whole) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) la_arrive_at(s_read[st]);
+        }
+        if (turn) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            va[j] = __float_as_uint(__uint_as_float(va[j]) * mult);
+            vb[j] = __float_as_uint(__uint_as_float(vb[j]) * mult);
+          }
+        }
+        if (!whole) {
+          bool bad = la_mask_row(va, static_cast<uint32_t>(vis));
+          if (hs == kLaHalf) {
+            bad |= la_mask_row(vb, static_cast<uint32_t>(vis >> 32));
+          } else {                                      // few rows: 16 columns, all among the first
+#pragma unroll
+            for (int j = 0; j < 32; ++j) vb[j] = 0xff800000u;
+          }
+          // A cache row that holds something not finite gives every query row of the pair a logit that is not
+          // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and
+          // each warp that does clears its CTA's staged values before its own arrival (two warps that clear the same
+          // piece store the same bytes).
+          if (__builtin_expect(__any_sync(0xffffffffu, bad), 0)) {
+            // a weight of 0 times a visible value that is not finite is NaN, as in a whole tile; here the divisor is
+            if (la_low_rows(P.latent, static_cast<int64_t>(kind ? w.rowd : w.row0) + a, scol, vis,
+                            P.scale < 0.f ? 0x7f800000u : 0xff800000u))
+              lt = __uint_as_float(0x7fffffffu);
+            if ((i > 0 && !la_wait(&bars->odone, (g - 1) & 1, abort_flag)) ||
+                !la_wait_read(&bars->v_seen, vn & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            la_acquire(&bars->v_seen, vn & 1);
+            for (int c = 0; c < 2; ++c) {
+              uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + c * kLaVGroup);
+              for (int e = lane; e < 2 * 8 * 2 * hs; e += 32) {
+                uint4 x = v4[e];
+                uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((xw[k] & 0x7f80u) == 0x7f80u) xw[k] &= 0xffff0000u;
+                  if ((xw[k] & 0x7f800000u) == 0x7f800000u) xw[k] &= 0x0000ffffu;
+                }
+                v4[e] = x;
+              }
+            }
+          }
+        }
+        if (!whole) {
+          ++vn;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) la_arrive_at(s_read[st]);
+        }
+        // the row's maximum: this thread's half and, from the other warp of the pair, the other half
+        float mt = la_row_max(va, vb, sl2);
+        xch[128 * st + tl] = mt;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->mx[grp]);
+        if (!la_wait_read(&bars->mx[grp], xn & 1, abort_flag)) { ok = false; break; }
+        ++xn;
+        mt = fmaxf(mt, xch[128 * st + (tl ^ 64)]);
+        const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
+        const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
+        if (grow) m = mt;
+        l *= f;
+        lt *= f;
+        const float ref = m == neg_inf() ? 0.f : m;
+        uint32_t pw[32];
+        la_row_weights(va, vb, sl2, ref, pw, l, lt);
+        if (i > 0) {
+          // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
+          if (!la_wait(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[32];
+              tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st_32x32(trow + kLaColO + 32 * c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights: row r of the K-major panel of 64 cache rows (128-byte swizzle), 8 rows a piece
+        uint8_t* prow = smem + kLaOffP + (hs == 64 ? half * kLaPanelBytes : 0) + r * 128;
+        if (hs == 64) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
+                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(prow + (((c + 2 * half) ^ (r & 7)) << 4)) =
+                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) la_arrive_at(pfull0);
+      }
+      // ------------------------------------------------------------ output
+      if (ok && nt > 0) ok = la_wait(&bars->odone, (g - 1) & 1, abort_flag);
+      if (ok && nt > 0) {
+        // the row's sums: the two threads' halves
+        tc_fence_after();
+        xsum[tl] = lt;
+        if (half) xsum[128 + r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->mx[grp]);
+        ok = la_wait_read(&bars->mx[grp], xn & 1, abort_flag);
+        ++xn;
+        lt += xsum[tl ^ 64];
+        if (!half) l += xsum[128 + r];
+      }
+      if (ok) {
+        // nothing visible (or only -inf logits): the rounded weights' sum is 0 exactly when that of the weights is
+        const bool empty = lt == 0.f;
+        const float inv = empty ? 0.f : 1.f / lt;
+        const int64_t row = static_cast<int64_t>(w.grow0) + rq;
+        const bool parts = w.part >= 0;
+        const int64_t part_row = static_cast<int64_t>(w.part) * kLaRows + rq;
+        if (half == 0 && live) {
+          // (a part that saw nothing but such rows is not empty: the join has to read its NaN)
+          const float v = empty ? neg_inf() : parts && l == 0.f ? lt : (m + log2f(l)) * 0.6931471805599453f;
+          if (parts)
+            P.part_lse[part_row] = v;
+          else if (P.lse)
+            P.lse[row] = v;
+        }
+        // Rows leave through the warp's 4 KB of the weights' place (free until its next weights), 128 bytes of each of
+        // its 32 rows at a time, so that a store covers four rows' whole lines.  Columns 32 c .. of this lane are
+        // value columns 256 (c / 4) + 128 half + 32 (c % 4) ...
+        const bool wide = parts || !P.out_bf16;
+        const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
+        const int64_t row0 = (parts ? static_cast<int64_t>(w.part) * kLaRows : static_cast<int64_t>(w.grow0)) +
+                             kLaHalf * cr + (quad & 1) * 32;
+        uint8_t* dst = parts ? reinterpret_cast<uint8_t*>(P.part_o) : static_cast<uint8_t*>(P.out);
+        dst += row0 * (kAttnValue * (wide ? 4 : 2));
+        uint8_t* stage = smem + kLaOffP + quad * 4096;
+        uint8_t* mine = stage + lane * 128;
+        // (rolled loops: this code runs once an item, and what it takes of the instruction cache the tiles' code
+        // misses)
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {
+          uint32_t x[32];
+          if (nt > 0) {
+            tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x);
+            tmem_wait_ld(x);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = 0u;
+          }
+          const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+          // (a row that saw nothing: its weights were 0 and its values finite, so the accumulator is 0)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * inv);
+          if (wide) {                                   // 32 columns are 128 bytes
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
+                  make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          } else {                                      // 64 columns are
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t p2[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 h =
+                    __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]), __uint_as_float(x[8 * k + 2 * e + 1]));
+                p2[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(mine + (((k + 4 * (c & 1)) ^ (lane & 7)) << 4)) =
+                  make_uint4(p2[0], p2[1], p2[2], p2[3]);
+            }
+          }
+          if (wide || (c & 1))
+            la_rows_out(stage, dst + (wide ? 4 * col : 2 * (col - 32)), kAttnValue * (wide ? 4 : 2), keep, lane);
+        }
+      }
+    }
+  } else if (warp == 0) {
     // ------------------------------------------------------------ items, query and key copies
     // Both CTAs copy their own halves; the first CTA's barriers count both (it alone announces the bytes).  All lanes
     // look for the next item, one hands it on and copies.
@@ -710,46 +974,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       if (P.cut && first) P.joins[blockIdx.x >> 1] = join;
       if (!ok) la_settle();
     }
-  } else if (warp == 7) {
-    // ------------------------------------------------------------ value copies
-    // (a warp of their own: their places become free at another pace than the keys')
-    if (lane == 0) {
-      const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
-      const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
-      bool ok = true;
-      int g = 0;
-      for (int ic = 0; ok; ++ic) {
-        const int slot = ic % kLaItems;
-        if (!mbar_wait<false>(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) { ok = false; break; }
-        const LaItem w = bars->item[slot];
-        mbar_arrive(&bars->item_empty[slot]);
-        if (w.nt < 0) break;
-        for (int i = 0; i < w.nt && ok; ++i, ++g) {
-          int kind, a, cnt;
-          w.sp.tile(w.i0 + i, kind, a, cnt);
-          const int box = la_box_rows(cnt);
-          const int row = (kind ? w.rowd : w.row0) + a;
-          for (int c = 0; c < 2; ++c) {
-            // output MMA c has value columns 256 c .. : this CTA's 128 are panels 4 c + 2 cr and the next
-            if (!mbar_wait<false>(&bars->v_empty[c], (g & 1) ^ 1, abort_flag)) { ok = false; break; }
-            if (cr == 0) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
-            la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
-                       4 * c + 2 * cr);
-          }
-          if (cr == 0 && ok && !w.sp.whole(kind, a, cnt, P.n_sink)) {
-            // both CTAs' softmax warps may read and clear these values; the other CTA's copies report to this one
-            // (this warp waits for the values' MMAs anyway: the MMA warp's tiles took 1000 cycles longer with it)
-            for (int c = 0; c < 2 && ok; ++c) {
-              ok = mbar_wait<false>(&bars->v_full[c], g & 1, abort_flag);
-              la_acquire(&bars->v_full[c], g & 1);
-            }
-            la_arrive_release(seen0);
-            la_arrive_release(seen1);
-          }
-        }
-      }
-      if (!ok) la_settle();
-    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ logit MMAs of the pair (first CTA)
     const uint32_t base = smem_u32(smem);
@@ -776,7 +1000,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         for (int c = 0; c < kLaKGroups; ++c) {
           if (!la_wait_all(&bars->k_full[c], g & 1, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t qd = qdesc + c * (kLaKPer * kLaPanelBytes / 16), kd = kdesc + c * (kLaKPer * kLaPanelBytes / 16);
+          const uint64_t qd = qdesc + c * (kLaKPer * kLaPanelBytes / 16);
+          const uint64_t kd = kdesc + c * (kLaKPer * kLaPanelBytes / 16);
           const uint32_t acc0 = c ? 1u : 0u;
           if (full) {
 #pragma unroll
@@ -859,259 +1084,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
       __syncwarp();
     }
   } else {
-    // ------------------------------------------------------------ softmax + epilogue
-    const int quad = warp & 3;                        // warps 3-6: tensor-memory lanes 32 * (warp & 3) ..
-    const int tl = quad * 32 + lane;                  // tensor-memory lane
-    const int r = tl & 63, half = tl >> 6;            // row of this CTA, and which half of a tile's rows
-    const int grp = quad & 1;                         // the two warps that share 32 rows
-    const int rq = kLaHalf * cr + r;                  // row of the pair
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    float* xch = reinterpret_cast<float*>(smem + kLaOffX);
-    const uint32_t pfull0 = la_map(&bars->pfull, 0);
-    // a pair without a run (fewer places than pairs) may lie between an item's parts: its own is empty
-    if (P.cut && cr == 0 && bars->idle)
-      P.part_lse[2 * static_cast<int64_t>(blockIdx.x >> 1) * kLaRows + tl] = neg_inf();
-    // logits in log2 units; a scale that is not above 0 turns (or clears) the logits first
-    const bool turn = !(P.scale > 0.f);
-    const float mult = P.scale < 0.f ? -1.f : 0.f;
-    const float sl2 = P.scale == 0.f ? 1.f : fabsf(P.scale) * 1.4426950408889634f;
-    bool ok = true;
-    const uint32_t s_read[2] = {la_map(&bars->s_empty[0], 0), la_map(&bars->s_empty[1], 0)};
-    float* xsum = reinterpret_cast<float*>(smem + kLaOffL);
-    int g = 0, xn = 0, vn = 0;                        // tiles, exchanges, tiles that are not whole
-    for (int ic = 0; ok; ++ic) {
-    LaItem w;
-    if (!la_next_item(bars, ic, w, abort_flag)) { ok = false; break; }
-    const LaSpan& sp = w.sp;
-    const int nt = __shfl_sync(0xffffffffu, w.nt, 0);
-    if (nt < 0) break;
-    const bool live = rq < w.nrows;
-    const int tok = (static_cast<uint32_t>(w.r0) + (live ? rq : w.nrows - 1)) / static_cast<uint32_t>(H);
-    // this row's visible rows of the sequence: [0, hi) cut by the sinks and the window
-    int hi, lo;
-    const uint64_t* branch = nullptr;
-    if (is_tree) {
-      branch = P.tree + static_cast<int64_t>(w.t0 + tok) * P.words;
-      int depth = 0;
-      if (P.window > 0) {
-        for (int c = 0; c < P.words; ++c) depth += __popcll(__ldg(branch + c) & la_low_mask(w.n - 64 * c));
-        depth = depth > 0 ? depth - 1 : 0;
-      }
-      hi = sp.hi;
-      lo = la_window_lo(w.kv + depth, P.window, P.align);
-    } else {
-      const int p = w.kv - w.n + tok;
-      hi = p + 1 < w.avail ? p + 1 : w.avail;
-      lo = la_window_lo(p, P.window, P.align);
-    }
-    float m = neg_inf(), l = 0.f, lt = 0.f;           // reference, sum of the weights, of the rounded weights
-    for (int i = 0; i < nt && ok; ++i, ++g) {
-      const int st = g & 1;
-      int kind, a0, cnt0;
-      sp.tile(w.i0 + i, kind, a0, cnt0);
-      const bool whole = sp.whole(kind, a0, cnt0, P.n_sink);
-      // this thread's rows of the tile: `hs` from a on, cnt of them in the tile
-      const int hs = la_box_rows(cnt0) / 2;
-      const int a = a0 + hs * half;
-      const int left = cnt0 - hs * half, cnt = left < 0 ? 0 : left < hs ? left : hs;
-      uint64_t vis = ~0ull;
-      if (!whole) {
-        if (kind == 0)
-          vis = la_low_mask(hi - a < cnt ? hi - a : cnt) & (la_low_mask(P.n_sink - a) | ~la_low_mask(lo - a));
-        else
-          vis = cnt > 0 ? (__ldg(branch + (a >> 6)) >> (a & 63)) & la_low_mask(cnt) : 0ull;
-      }
-      if (!la_wait(&bars->sfull[st], (g >> 1) & 1, abort_flag)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t va[32], vb[32];
-      const uint32_t scol = trow + kLaColS + 64 * st;
-      tmem_ld_32x32_nowait(scol, va);
-      tmem_ld_32x32_nowait(scol + 32, vb);
-      tmem_wait_ld(va);
-      tmem_wait_ld(vb);
-      if (whole) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) la_arrive_at(s_read[st]);
-      }
-      if (turn) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          va[j] = __float_as_uint(__uint_as_float(va[j]) * mult);
-          vb[j] = __float_as_uint(__uint_as_float(vb[j]) * mult);
-        }
-      }
-      if (!whole) {
-        bool bad = la_mask_row(va, static_cast<uint32_t>(vis));
-        if (hs == kLaHalf) {
-          bad |= la_mask_row(vb, static_cast<uint32_t>(vis >> 32));
-        } else {                                      // few rows: 16 columns, all among the first
-#pragma unroll
-          for (int j = 0; j < 32; ++j) vb[j] = 0xff800000u;
-        }
-        // A cache row that holds something not finite gives every query row of the pair a logit that is not
-        // finite, so both CTAs find out (the tile's values have landed after the output before it is complete), and each warp that does clears its CTA's staged values before its own
-        // arrival (two warps that clear the same piece store the same bytes).
-        if (__any_sync(0xffffffffu, bad)) {
-          // a weight of 0 times a visible value that is not finite is NaN, as in a whole tile: here the row's divisor is
-          if (la_low_rows(P.latent, static_cast<int64_t>(kind ? w.rowd : w.row0) + a, scol, vis,
-                          P.scale < 0.f ? 0x7f800000u : 0xff800000u))
-            lt = __uint_as_float(0x7fffffffu);
-          if ((i > 0 && !la_wait(&bars->odone, (g - 1) & 1, abort_flag)) ||
-              !la_wait_read(&bars->v_seen, vn & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          la_acquire(&bars->v_seen, vn & 1);
+    // ------------------------------------------------------------ value copies
+    // (a warp of their own: their places become free at another pace than the keys')
+    if (lane == 0) {
+      const uint32_t v_full[2] = {la_map(&bars->v_full[0], 0), la_map(&bars->v_full[1], 0)};
+      const uint32_t seen0 = la_map(&bars->v_seen, 0), seen1 = la_map(&bars->v_seen, 1);
+      bool ok = true;
+      int g = 0;
+      for (int ic = 0; ok; ++ic) {
+        const int slot = ic % kLaItems;
+        if (!mbar_wait<false>(&bars->item_full[slot], (ic / kLaItems) & 1, abort_flag)) { ok = false; break; }
+        const LaItem w = bars->item[slot];
+        mbar_arrive(&bars->item_empty[slot]);
+        if (w.nt < 0) break;
+        for (int i = 0; i < w.nt && ok; ++i, ++g) {
+          int kind, a, cnt;
+          w.sp.tile(w.i0 + i, kind, a, cnt);
+          const int box = la_box_rows(cnt);
+          const int row = (kind ? w.rowd : w.row0) + a;
           for (int c = 0; c < 2; ++c) {
-            uint4* v4 = reinterpret_cast<uint4*>(smem + kLaOffV + c * kLaVGroup);
-            for (int e = lane; e < 2 * 8 * 2 * hs; e += 32) {
-              uint4 x = v4[e];
-              uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((xw[k] & 0x7f80u) == 0x7f80u) xw[k] &= 0xffff0000u;
-                if ((xw[k] & 0x7f800000u) == 0x7f800000u) xw[k] &= 0x0000ffffu;
-              }
-              v4[e] = x;
+            // output MMA c has value columns 256 c .. : this CTA's 128 are panels 4 c + 2 cr and the next
+            if (!mbar_wait<false>(&bars->v_empty[c], (g & 1) ^ 1, abort_flag)) { ok = false; break; }
+            if (cr == 0) mbar_arrive_expect_tx(&bars->v_full[c], 2 * 2 * box * 128);
+            la_load_3d(smem + kLaOffV + c * kLaVGroup, box == kLaTile ? &M.v : &M.v_few, v_full[c], row,
+                       4 * c + 2 * cr);
+          }
+          if (cr == 0 && ok && !w.sp.whole(kind, a, cnt, P.n_sink)) {
+            // both CTAs' softmax warps may read and clear these values; the other CTA's copies report to this one
+            // (this warp waits for the values' MMAs anyway: the MMA warp's tiles took 1000 cycles longer with it)
+            for (int c = 0; c < 2 && ok; ++c) {
+              ok = mbar_wait<false>(&bars->v_full[c], g & 1, abort_flag);
+              la_acquire(&bars->v_full[c], g & 1);
             }
+            la_arrive_release(seen0);
+            la_arrive_release(seen1);
           }
         }
       }
-      if (!whole) {
-        ++vn;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) la_arrive_at(s_read[st]);
-      }
-      // the row's maximum: this thread's half and, from the other warp of the pair, the other half
-      float mt = la_row_max(va, vb, sl2);
-      xch[128 * st + tl] = mt;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      if (!la_wait_read(&bars->mx[grp], xn & 1, abort_flag)) { ok = false; break; }
-      ++xn;
-      mt = fmaxf(mt, xch[128 * st + (tl ^ 64)]);
-      const bool grow = mt > m + kLaLazy;             // true at the first visible finite logit
-      const float f = grow ? (m == neg_inf() ? 0.f : la_exp2(m - mt)) : 1.f;
-      if (grow) m = mt;
-      l *= f;
-      lt *= f;
-      const float ref = m == neg_inf() ? 0.f : m;
-      uint32_t pw[32];
-      la_row_weights(va, vb, sl2, ref, pw, l, lt);
-      if (i > 0) {
-        // the output of the tile before is complete: its weights are read and its accumulator may be rescaled
-        if (!la_wait(&bars->odone, (g - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[32];
-            tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st_32x32(trow + kLaColO + 32 * c, o);
-          }
-          tmem_wait_st();
-        }
-      }
-      // weights: row r of the K-major panel of 64 cache rows (128-byte swizzle), 8 rows a piece
-      uint8_t* prow = smem + kLaOffP + (hs == 64 ? half * kLaPanelBytes : 0) + r * 128;
-      if (hs == 64) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
-              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<uint4*>(prow + (((c + 2 * half) ^ (r & 7)) << 4)) =
-              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) la_arrive_at(pfull0);
-    }
-    // ------------------------------------------------------------ output
-    if (ok && nt > 0) ok = la_wait(&bars->odone, (g - 1) & 1, abort_flag);
-    if (ok && nt > 0) {
-      // the row's sums: the two threads' halves
-      tc_fence_after();
-      xsum[tl] = lt;
-      if (half) xsum[128 + r] = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->mx[grp]);
-      ok = la_wait_read(&bars->mx[grp], xn & 1, abort_flag);
-      ++xn;
-      lt += xsum[tl ^ 64];
-      if (!half) l += xsum[128 + r];
-    }
-    if (ok) {
-      // nothing visible (or only -inf logits): the sum of the rounded weights is 0 exactly when that of the weights is
-      const bool empty = lt == 0.f;
-      const float inv = empty ? 0.f : 1.f / lt;
-      const int64_t row = static_cast<int64_t>(w.grow0) + rq;
-      const bool parts = w.part >= 0;
-      const int64_t part_row = static_cast<int64_t>(w.part) * kLaRows + rq;
-      if (half == 0 && live) {
-        // (a part that saw nothing but such rows is not empty: the join has to read its NaN)
-        const float v = empty ? neg_inf() : parts && l == 0.f ? lt : (m + log2f(l)) * 0.6931471805599453f;
-        if (parts)
-          P.part_lse[part_row] = v;
-        else if (P.lse)
-          P.lse[row] = v;
-      }
-      // Rows leave through the warp's 4 KB of the weights' place (free until its next weights), 128 bytes of each of
-      // its 32 rows at a time, so that a store covers four rows' whole lines.  Columns 32 c .. of this lane are
-      // value columns 256 (c / 4) + 128 half + 32 (c % 4) ...
-      const bool wide = parts || !P.out_bf16;
-      const uint32_t keep = __ballot_sync(0xffffffffu, live && !(parts && empty));   // an empty part is not read
-      const int64_t row0 = (parts ? static_cast<int64_t>(w.part) * kLaRows : static_cast<int64_t>(w.grow0)) + kLaHalf * cr + (quad & 1) * 32;
-      uint8_t* dst = parts ? reinterpret_cast<uint8_t*>(P.part_o) : static_cast<uint8_t*>(P.out);
-      dst += row0 * (kAttnValue * (wide ? 4 : 2));
-      uint8_t* stage = smem + kLaOffP + quad * 4096;
-      uint8_t* mine = stage + lane * 128;
-      // (rolled loops: this code runs once an item, and what it takes of the instruction cache the tiles' code misses)
-#pragma unroll 2
-      for (int c = 0; c < 8; ++c) {
-        uint32_t x[32];
-        if (nt > 0) {
-          tmem_ld_32x32_nowait(trow + kLaColO + 32 * c, x);
-          tmem_wait_ld(x);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = 0u;
-        }
-        const int col = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
-        // (a row that saw nothing: its weights were 0 and its values finite, so the accumulator is 0)
-#pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * inv);
-        if (wide) {                                   // 32 columns are 128 bytes
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(mine + ((k ^ (lane & 7)) << 4)) =
-                make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-        } else {                                      // 64 columns are
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t p2[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 h =
-                  __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * e]), __uint_as_float(x[8 * k + 2 * e + 1]));
-              p2[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(mine + (((k + 4 * (c & 1)) ^ (lane & 7)) << 4)) =
-                make_uint4(p2[0], p2[1], p2[2], p2[3]);
-          }
-        }
-        if (wide || (c & 1))
-          la_rows_out(stage, dst + (wide ? 4 * col : 2 * (col - 32)), kAttnValue * (wide ? 4 : 2), keep, lane);
-      }
-    }
+      if (!ok) la_settle();
     }
   }
 
