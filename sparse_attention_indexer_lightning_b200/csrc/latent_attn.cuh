@@ -480,8 +480,8 @@ __device__ __forceinline__ bool la_item(const LatentAttnParams& P, int b, int qt
 // another.  Lane i holds the places of sequence b0 + i, so that sequences without tokens (a padded batch has many) are
 // stepped over 32 at a time.
 //
-// Whole items: one place per item; pair p takes the places p, p + pairs, ...  (Of one sequence, or a few sequences of
-// one item at most, the places are counted without a look at the tables, and some may have no item.)
+// Whole items: one place per item; pair p takes the places p, p + pairs, ...  (Of one sequence, or as many sequences of
+// one item at most as there are pairs, the places are counted without a look at the tables, and some have no item.)
 //
 // Cut: every sequence's items weigh its last one's tiles and kLaItemCost; of the sum of all, pair p takes the places
 // total * p / pairs .. total * (p + 1) / pairs.  Place x of an item is its tile x - kLaItemCost (the first places are
@@ -498,7 +498,7 @@ struct LaIter {
     lane = lane_;
     pairs = static_cast<int>(gridDim.x >> 1);
     const int64_t p = blockIdx.x >> 1;
-    guess = !P.cut && (P.B == 1 || (P.max_tiles == 1 && P.B <= 4 * pairs));
+    guess = !P.cut && (P.B == 1 || (P.max_tiles == 1 && P.B <= pairs));
     base = total = item_end = 0;
     pos = p;
     end = INT64_MAX;
