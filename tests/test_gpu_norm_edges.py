@@ -1,6 +1,7 @@
-"""fp8 rows of tiny values from the norm and rotation (CUDA, through the C ABI), against fp64.
+"""The norm and rotation at the edges of its range: fp8 rows of tiny values, and every kernel form with what it
+specialises (CUDA, through the C ABI), against fp64.
 
-Tolerances: the fp8 scale of a tiny row is an fp32 number
+Tolerances: those of test_gpu_norm_rope.py for rows of ordinary size.  The fp8 scale of a tiny row is an fp32 number
 that may be subnormal, so it is within an ulp or two (2^-22 of itself) and half the smallest step (2^-150) of max |y| /
 448; a code is held against y over the scale that was returned: half an e4m3 step, 2^-4 of the quotient or 2^-10, and
 1e-5 of it for the quotient's own fp32 rounding.
@@ -10,7 +11,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_norm_rope import L  # noqa: F401
+from oracle.attention import norm_rope
+from test_gpu_norm_rope import L, check, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,30 @@ def test_fp8_rows_of_tiny_values_rotated_and_normed(L):  # noqa: F811
         # y itself is rounded to a multiple of 2^-149, the scale too; a code is half an e4m3 step off at most
         assert abs(s - max(val / 448, 2.0 ** -149)) <= 2.0 ** -150 + 2.0 ** -149 / 448 + 1e-6 * s, w
         assert torch.all((c[:64] * s - val).abs() <= 2.0 ** -149 + 2.0 ** -4 * val + 2.0 ** -10 * s), w
+
+
+SHAPES = [
+    # d, norm_dim, rope, rope_off: one, two, three, four and nine pieces a lane, the rotated part in the first, a middle
+    # and the last step, across two steps, and at odd offsets
+    (256, 256, 64, 0), (256, 256, 64, 192), (256, 128, 256, 0), (256, 256, 64, 101),
+    (512, 512, 64, 0), (512, 512, 64, 256), (512, 512, 64, 448), (512, 512, 64, 224), (512, 448, 64, 3),
+    (320, 320, 64, 0), (320, 320, 64, 128), (320, 320, 64, 256), (264, 264, 8, 256),
+    (192, 192, 64, 0), (192, 192, 64, 64), (192, 128, 64, 128), (192, 192, 64, 32), (136, 136, 32, 104),
+    (576, 576, 64, 0), (576, 512, 64, 480), (1024, 1024, 64, 224), (1024, 1024, 256, 256), (1024, 1000, 64, 960),
+    (128, 128, 128, 0), (120, 120, 48, 72), (64, 32, 16, 48),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=["-".join(map(str, s)) for s in SHAPES])
+def test_every_form(L, shape, interleaved, fp8):  # noqa: F811
+    d, nd, rope, off = shape
+    s = make(9, 5, 2, d, rope, nd, seed=d + off)
+    out = L.ls_norm_rope(s["q"], s["k"], s["pos"], s["inv_freq"], q_norm="rms", k_norm="layer", norm_dim=nd,
+                         q_weight=s["qw"], k_weight=s["kw"], k_bias=s["kb"], eps=1e-5, rope_off=off,
+                         interleaved=interleaved, fp8=fp8)
+    c = lambda t: None if t is None else t.double().cpu().numpy()  # noqa: E731
+    for x, norm, w, b, y, sc, name in ((s["q"], "rms", s["qw"], None, out[0], out[1], "q"),
+                                       (s["k"], "layer", s["kw"], s["kb"], out[2], out[3], "k")):
+        check(y, sc, norm_rope(c(x), c(s["pos"]), c(s["inv_freq"]), norm, nd, c(w), c(b), 1e-5, off, interleaved), name)

@@ -1,6 +1,7 @@
-"""The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: n_sink at the largest int,
-batches whose max_q is left at its default, more tokens than max_q, logits that are not finite, the read lists of
-the LSA search.  Tolerances as in test_gpu_span_attention.py.
+"""The span attentions at their edges (CUDA, through the C ABI), against the fp64 oracle: maxima that grow from tile to
+tile, sinks of several tiles, n_sink at the largest int, pairs that run through many items, batches whose max_q is
+left at its default, more tokens than max_q, logits that are not finite, the read lists of the LSA search.
+Tolerances as in test_gpu_span_attention.py.
 """
 
 import numpy as np
@@ -15,11 +16,83 @@ from workloads.synth import make_lsa
 
 pytestmark = pytest.mark.gpu
 
+FACTORS = (1.0, 0.75, 0.5, -1.0, 0.0, -0.25, 2.0)
+
+
+def levels(d, level):
+    """Logits that follow `level` (one number per latent row) times a factor of the head, in nats: column 512 holds the
+    level and the query 24 times the factor (the scale is 1 / 24); values and the other logits as they were."""
+    lat = d["lat"].double()
+    lat[:, 512:] = 0.0
+    lat[:level.shape[0], 512] = torch.from_numpy(level)
+    d["lat"] = lat.to(torch.bfloat16)
+    assert torch.equal(d["lat"][:level.shape[0], 512].double(), torch.from_numpy(level)), "levels that bf16 rounds"
+    q = d["q"].double()
+    q[:, :, 512:] = 0.0
+    q[:, :, 512] = 24.0 * torch.tensor([FACTORS[h % len(FACTORS)] for h in range(d["H"])])
+    d["q"] = q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ctx,drafted", [(450, 3), (512, 3), (385, 40), (640, 1), (130, 3)])
+def test_maxima_that_grow_from_tile_to_tile(L, ctx, drafted, dtype):  # noqa: F811
+    """16 nats a tile (23 in log2: above the 16 that force a rescale), 12 (17), 8 (11.5: every second tile), falling, flat,
+    and 32: the output is rescaled in full tiles, in a tile of few rows and in the tile of the drafted rows.  max_ctx = 1
+    keeps the item whole (the hint decides the split only)."""
+    d = make([drafted], [ctx], 16, "marks", seed=ctx, drafted=True)
+    levels(d, 16.0 * (np.arange(ctx + drafted) // 128 + (np.arange(ctx + drafted) >= ctx)))
+    branches = random_tree(d["rng"], d["ns"])
+    rows = d["lat"].shape[0]
+    assert L.lib().ls_tree_attention_workspace_size(1, drafted, 16, drafted, rows, 1, 0, 1, 0) == 0
+    tree(L, d, branches, "marks", dtype=dtype, max_ctx=1)
+    tree(L, d, branches, "marks", dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_maxima_that_grow_in_whole_windows(L, dtype):  # noqa: F811
+    """As many query tiles as pairs, so that each pair has one whole item: window tiles that grow, then sinks above all of
+    them (the sinks come last)."""
+    d = make([74], [700], 128, "marks", seed=31)
+    level = 16.0 * (np.arange(700) // 128)
+    level[:4] = 128.0
+    levels(d, level)
+    assert L.lib().ls_window_attention_workspace_size(1, 74, 128, 74, 500, 1, 4) == 0
+    window(L, d, 500, 1, 4, "marks", dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_maxima_that_grow_inside_cut_runs(L, dtype):  # noqa: F811
+    """One item over all pairs, four tiles a run, levels that rise over five tiles and start again."""
+    ctx = 74 * 4 * 128 + 50
+    d = make([1], [ctx], 16, "marks", seed=32, drafted=True)
+    levels(d, 16.0 * (np.arange(ctx + 1) // 128 % 5))
+    need = L.lib().ls_tree_attention_workspace_size(1, 1, 16, 1, d["lat"].shape[0], ctx, 0, 1, 0)
+    assert need > 2 * 74 * 128 * 512 * 4                  # all 74 pairs
+    tree(L, d, [{0}], "marks", dtype=dtype, max_ctx=ctx)
+
+
+@pytest.mark.parametrize("sinks", [128, 200, 256, 300])
+def test_sinks_of_several_tiles(L, sinks):  # noqa: F811
+    d = make([40], [1200], 16, "marks", seed=sinks)
+    window(L, d, 100, 1, sinks, "marks")
+    d = make([74], [1200], 128, "random", seed=sinks)     # whole items
+    window(L, d, 100, 1, sinks, "random", dtype=torch.float32)
+    d = make([20], [900], 16, "marks", seed=sinks, drafted=True)
+    tree(L, d, random_tree(d["rng"], [20]), "marks", window=128, n_sink=sinks)
+
 
 def test_all_sinks(L):  # noqa: F811
     """n_sink at the largest int: every row is one."""
     d = make([3], [300], 16, "marks", seed=33)
     window(L, d, 1, 1, (1 << 31) - 1, "marks")
+
+
+@pytest.mark.parametrize("n,H", [(500, 128), (1500, 40)])
+def test_pairs_that_run_through_many_items(L, n, H):  # noqa: F811
+    """Six or seven whole items a pair, so that the places of the items in shared memory come round."""
+    d = make([n], [n + 20], H, "random", seed=n)
+    assert L.lib().ls_window_attention_workspace_size(1, n, H, n, 20, 1, 4) == 0
+    window(L, d, 20, 1, 4)
 
 
 def best_us(call, n=20, tries=4):
