@@ -739,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
           __syncwarp();
           if (lane == 0) la_arrive_at(s_read[st]);
         }
-        if (turn) {
+        if (__builtin_expect(turn, 0)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             va[j] = __float_as_uint(__uint_as_float(va[j]) * mult);
@@ -825,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         }
         // weights: row r of the K-major panel of 64 cache rows (128-byte swizzle), 8 rows a piece
         uint8_t* prow = smem + kLaOffP + (hs == 64 ? half * kLaPanelBytes : 0) + r * 128;
-        if (hs == 64) {
+        if (__builtin_expect(hs == 64, 1)) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) =
@@ -952,6 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
         if (ok && w.nt > 0) {
           ++qn;
           if (first) mbar_arrive_expect_tx(&bars->qfull, 2 * kLaPanels * kLaPanelBytes);
+#pragma unroll 1
           for (int c = 0; c < kLaKGroups; ++c)
             la_load_3d(smem + c * kLaKPer * kLaPanelBytes, &M.q, qfull, w.grow0 + kLaHalf * cr, kLaKPer * c);
           for (int i = 0; i < w.nt && ok; ++i) {
