@@ -591,11 +591,13 @@ ls_status ls_tree_attention(const uint16_t* q, const uint16_t* latent, const int
  *   slots [T] int64 or NULL: the output row of token t, for a cache of
  *        out_rows rows; -1 writes nothing.  Other rows are left as they are;
  *        a slot outside [-1, out_rows) writes nothing and sets
- *        LS_FAULT_BAD_INDEX; of two tokens with one slot either may win.
- *        NULL: row t.
+ *        LS_FAULT_BAD_INDEX; two tokens with one slot may leave a mix of
+ *        both in that row and its scale.  NULL: row t.
  * x and out must not overlap.  d a multiple of 8 up to 1024, norm_dim a
  * multiple of 8 in [8, d] (0 without a norm), rope_dim even in [0, 256],
  * rope_off + rope_dim <= d.  pos [T] int64, inv_freq [rope_dim / 2] fp32.
+ * A norm's sum of squares is in fp32: rows whose largest magnitude is above
+ * 2^58, or with eps = 0 below 2^-58, leave its range.
  * x, out 16-byte aligned.  No workspace.
  */
 #define LS_NORM_NONE 0

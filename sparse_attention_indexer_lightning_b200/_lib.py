@@ -830,9 +830,9 @@ def ls_norm_rope(q=None, k=None, pos=None, inv_freq=None, q_norm: str = "none", 
     biases [norm_dim] f32; pos [T] int64 and inv_freq [rope/2] f32 rotate the elements from rope_off on, in pairs
     (2i, 2i+1) when interleaved, else (i, i + rope/2); inv_freq None: no rotation.
     k_cache [R,Hk,d] or, Hk = 1, [R,d] (bf16 or float8_e4m3fn) with slots [T] int64 takes the keys at rows slots[t]
-    (-1: nowhere), k_scale [R,Hk] or [R] f32 the scales of an fp8 cache.  fp8 (default: k_cache's type, else False)
-    asks for codes and scales.  -> (q_out [T,Hq,d], q_scale [T,Hq] or None, k_out, k_scale or None); k_out is k_cache
-    when that is given."""
+    (-1: nowhere; no other slot twice, or its row is a mix of two tokens), k_scale [R,Hk] or [R] f32 the scales of an
+    fp8 cache.  fp8 (default: k_cache's type, else False) asks for codes and scales.  -> (q_out [T,Hq,d], q_scale
+    [T,Hq] or None, k_out, k_scale or None); k_out is k_cache when that is given."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("ls_norm_rope needs q or k")

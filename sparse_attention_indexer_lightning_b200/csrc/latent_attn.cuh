@@ -63,11 +63,11 @@
 // workspace, at most two parts a pair, and latent_attn_combine_kernel joins
 // them.
 //
-// Measured on a B200 (GPU time): 4096 tokens x 128 heads over 4 + 512 rows 742
-// us (793 TFLOP/s); 16 drafted tokens x 128 heads over 32768 rows 122 us with
-// the join (1.2 PFLOP/s; a tile about 3000 cycles, the four softmax steps of a
-// row in a chain, where its MMAs take 2180); 64 single tokens x 128 heads 22
-// us.
+// Measured on a B200 (GPU time after a rest, below the power cap): 4096 tokens
+// x 128 heads over 4 + 512 rows 769 us (766 TFLOP/s); 16 drafted tokens x 128
+// heads over 32768 rows 139 us with the join (1.05 PFLOP/s; a tile about 4000
+// cycles, the four softmax steps of a row in a chain, where its MMAs take
+// 2180); 64 single tokens x 128 heads 22 us.
 
 #pragma once
 
@@ -88,8 +88,8 @@ constexpr int kLaVGroup = 2 * kLaTile * 128;          // 32 KB: two value panels
 constexpr int kLaThreads = 8 * 32;
 constexpr int kLaColO = 0, kLaColS = 256;             // tensor-memory columns
 constexpr float kLaLazy = 16.f;                       // log2 growth of a maximum that forces a rescale
-// An item's own cost in tiles: its query, its output (alone about four).  Of 1 to 5 in cut batches of long and short
-// contexts, 2 took 2 to 4 percent longer than 3, and 4 as long as 3, but 4 also cuts 5 tokens over 100 rows (17 us for 14).
+// An item's own cost in tiles: its query, its output.  Of 1 to 5 in cut batches of long and short contexts, 2 took 2 to
+// 4 percent longer than 3, and 4 as long as 3, but 4 also cuts 5 tokens over 100 rows (17 us for 14).
 constexpr int kLaItemCost = 3;
 
 // First row of the window of the token at position p.
@@ -591,9 +591,9 @@ __device__ __forceinline__ bool la_next_item(LaBars* bars, int ic, LaItem& w, vo
 // logits are on their way while the output of the last one leaves.  Barrier phases follow counts that run on over the
 // items: tiles (g), items with tiles (qn), exchanges (xn).
 //
-// The order of the roles in the source, and which branches are named rare, change where the tiles' loops lie in the code
-// and nothing else, but over 12 orders 16 tokens x 128 heads over 32768 rows took 132 to 164 us and 4096 tokens over a
-// window of 512 rows 763 to 821.  This order had the lowest mean over the cases.
+// The order of the roles in the source, which branches are named rare and which short loops are rolled change where the
+// tiles' loops lie in the code and nothing else, but over some 60 forms 16 tokens x 128 heads over 32768 rows took 131
+// to 164 us and 4096 tokens over a window of 512 rows 748 to 830.  This one had the lowest mean over the cases.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLaThreads, 1)
     latent_attn_kernel(const __grid_constant__ LaMaps M, const __grid_constant__ LatentAttnParams P) {
   extern __shared__ __align__(1024) uint8_t la_raw[];

@@ -12,10 +12,11 @@
 //          for the pairs (2i, 2i + 1), interleaved, or (i, i + rope / 2)
 //   fp8: scale = max |y| / 448 (1 for a row of zeros, else 2^-149 at least), code = e4m3(y / scale)
 //
-// Bound by bytes: every element is read and written once; what has to stay
-// small beside them is the number of instructions per row.  LPR lanes (8, 16
-// or 32, whichever leaves the fewest idle) share a row, each holding STEPS
-// pieces of 8 elements in fp32 between the passes that a norm needs.  A block
+// Long rows are bound by bytes: every element is read and written once; short
+// ones by the wait for a batch of rows and the instructions that follow.  LPR
+// lanes (8, 16 or 32, whichever leaves the fewest idle) share a row, each
+// holding STEPS pieces of 8 elements in fp32 between the passes that a norm
+// needs.  A block
 // works on heads of one token: its angles are formed once (in 64 bits: at a
 // position of ten million an fp32 product is off by a radian; reduced to half
 // turns before the fp32 sine and cosine), and a lane keeps those of its pieces
@@ -26,7 +27,8 @@
 //
 // Measured on a B200: 2048 x 129 rows of 576 elements 111 us, 5.5 TB/s (0.84 of
 // the measured copy); 4096 x 33 rows of 128 elements to fp8 22 us (2.5 TB/s:
-// 14 M warp instructions, the issue slots half used).
+// 14 M warp instructions, the issue slots half used: neither bytes nor issue
+// slots bound it, a warp loads its rows and works on them in turn).
 
 #pragma once
 
