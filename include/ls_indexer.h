@@ -520,9 +520,9 @@ ls_status ls_attention_merge(const float* o_parts, const float* lse_parts, int S
  * contraction rounded to bf16 (an output is within 2^-8 of the largest
  * visible value magnitude before its own rounding).
  * Faults: a q_start that is not ascending in [0, T], a sequence of more than
- * max_q tokens, a negative kv_len or rows outside [0, n_rows) set
- * LS_FAULT_BAD_INDEX; tokens past max_q may be left as they are, rows outside
- * the cache are not read and weigh nothing.
+ * max_q tokens, and of a sequence with tokens a negative kv_len or rows
+ * outside [0, n_rows) set LS_FAULT_BAD_INDEX; tokens past max_q may be left as
+ * they are, rows outside the cache are not read and weigh nothing.
  * Workspace: ls_window_attention_workspace_size() bytes: parts of the query rows
  * whose work is spread over several CTAs (at most 39 MB; 0 when whole tiles of
  * query rows fill the machine evenly); calls that overlap on the GPU, replays

@@ -16,14 +16,13 @@
 // ones by the wait for a batch of rows and the instructions that follow.  LPR
 // lanes (8, 16 or 32, whichever leaves the fewest idle) share a row, each
 // holding STEPS pieces of 8 elements in fp32 between the passes that a norm
-// needs.  A block
-// works on heads of one token: its angles are formed once (in 64 bits: at a
-// position of ten million an fp32 product is off by a radian; reduced to half
-// turns before the fp32 sine and cosine), and a lane keeps those of its pieces
-// in registers for all its rows.  Where the rotated part is whole pieces of
-// one step (ALIGNED), a rotation's partners are in the same piece
-// (interleaved) or in the same registers of another lane, one shuffle away;
-// any other offset goes through a strip of shared memory.
+// needs.  A block works on heads of one token: its angles are formed once (in
+// 64 bits: at a position of ten million an fp32 product is off by a radian;
+// reduced to half turns before the fp32 sine and cosine), and a lane keeps
+// those of its pieces in registers for all its rows.  Where the rotated part is
+// whole pieces of one step (ALIGNED), a rotation's partners are in the same
+// piece (interleaved) or in the same registers of another lane, one shuffle
+// away; any other offset goes through a strip of shared memory.
 //
 // Measured on a B200: 2048 x 129 rows of 576 elements 111 us, 5.5 TB/s (0.84 of
 // the measured copy); 4096 x 33 rows of 128 elements to fp8 22 us (2.5 TB/s:
