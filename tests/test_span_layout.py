@@ -33,3 +33,9 @@ def test_sinks_up_to_the_largest_int(lib):  # noqa: F811
     size = lambda n: lib.ls_window_attention_workspace_size(1, 3, 16, 3, 512, 1, n)  # noqa: E731
     assert size(big) == size(big - 500) == size(1 << 24) > 0
     assert window(lib, sink=big) == 2 and window(lib, sink=big - 500) == 2
+
+
+def test_short_windows_stay_whole(lib):  # noqa: F811
+    """Fewer query tiles than pairs with a few tiles each are dealt out whole, with one launch and no workspace."""
+    for B, n, H in ((32, 8, 16), (1, 30, 128), (40, 1, 128), (64, 1, 128)):
+        assert lib.ls_window_attention_workspace_size(B, B * n, H, n, 512, 1, 4) == 0
