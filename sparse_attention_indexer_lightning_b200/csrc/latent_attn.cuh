@@ -64,8 +64,8 @@
 // them.
 //
 // Measured on a B200 (GPU time after a rest, below the power cap): 4096 tokens
-// x 128 heads over 4 + 512 rows 769 us (766 TFLOP/s); 16 drafted tokens x 128
-// heads over 32768 rows 139 us with the join (1.05 PFLOP/s; a tile about 4000
+// x 128 heads over 4 + 512 rows 779 us (756 TFLOP/s); 16 drafted tokens x 128
+// heads over 32768 rows 138 us with the join (1.06 PFLOP/s; a tile about 4000
 // cycles, the four softmax steps of a row in a chain, where its MMAs take
 // 2180); 64 single tokens x 128 heads 22 us.
 
